@@ -272,6 +272,115 @@ swimba_status swimba_ssd_scan_bwd(const swimba_dims* dims, const void* Bpi, cons
  * aligned (SWIMBA_ERR_INVALID_ARG otherwise). */
 swimba_status swimba_out_proj(const swimba_dims* dims, const void* y, const void* w_out, void* out, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Operators around the token mixer: layer norm, the per-channel gated recurrence and the gated feed-forward
+ * block, each with its gradients.  They take dims of their own (below); the conventions at the head of this
+ * file hold, with these additions:
+ *  - dtype may be SWIMBA_F32, SWIMBA_BF16 or SWIMBA_F16; sums, statistics, states and gates are fp32.
+ *  - A row stride of 0 means dense rows; a larger one reads a slice of wider rows (the base pointer still
+ *    16-byte aligned).  Every other tensor is dense.
+ *  - grad_dtype is the dtype of the gradients that enter and leave: SWIMBA_F32, or dtype.
+ *  - Outputs may not overlap inputs, except where an entry point says so.
+ *  - The calls use no memory of the library's own: calls on different streams may overlap as long as their
+ *    outputs and workspaces do not, and every call can be captured into a CUDA graph. */
+
+typedef struct {
+  int32_t rows;       /* M */
+  int32_t width;      /* D: 1 .. 16384 */
+  int32_t dtype;      /* x, residual, r and y */
+  int32_t grad_dtype; /* dy, dr and dx */
+  int64_t x_stride;   /* elements between rows of x (0: width) */
+  float eps;          /* > 0, added to the variance */
+} swimba_norm_dims;
+
+/* Layer norm of x, or of the residual sum:
+ *   r = x + residual (r = x without residual),  y = (r - mean(r)) / sqrt(var(r) + eps) * gamma + beta
+ *   x [M][D] rows x_stride apart; residual [M][D] dtype or NULL; gamma, beta [D] fp32 or NULL (1 and 0)
+ *   y [M][D] dtype out; r_out [M][D] dtype out or NULL: the sum, rounded (y is normalised from the fp32 sum)
+ * var is the mean of the squared deviations.  r_out may be residual (the residual stream updated in place). */
+swimba_status swimba_layer_norm(const swimba_norm_dims* dims, const void* x, const void* residual, const float* gamma,
+                                const float* beta, void* y, void* r_out, void* stream);
+
+/* Bytes of workspace swimba_layer_norm_bwd needs (0 if the dims are invalid or unsupported). */
+size_t swimba_layer_norm_bwd_workspace_size(const swimba_norm_dims* dims);
+
+/* Gradients of swimba_layer_norm at the stored r, for L = sum <dy, y> (+ <dr, r>):
+ *   r [M][D] dtype (dense: x_stride is not read); gamma [D] fp32 or NULL; dy [M][D] grad_dtype
+ *   dr [M][D] grad_dtype or NULL: the gradient that reaches r past the norm, added to dx
+ *   dx [M][D] grad_dtype out: the gradient of r, hence of x and of residual; may be dy or dr
+ *   dgamma, dbeta [D] fp32 out, each or NULL: summed over the rows in a fixed order
+ * ws must hold swimba_layer_norm_bwd_workspace_size(dims) bytes. */
+swimba_status swimba_layer_norm_bwd(const swimba_norm_dims* dims, const void* r, const float* gamma, const void* dy,
+                                    const void* dr, void* dx, float* dgamma, float* dbeta, void* ws, size_t ws_bytes,
+                                    void* stream);
+
+typedef struct {
+  int32_t batch;      /* B */
+  int32_t seqlen;     /* T (1 for swimba_gated_step) */
+  int32_t width;      /* W: channels */
+  int32_t dtype;      /* x, gate and h */
+  int32_t grad_dtype; /* dh, dx and dgate */
+  int64_t x_stride;   /* elements between tokens of x (0: width) */
+  int64_t gate_stride;
+} swimba_gated_dims;
+
+/* The gated linear recurrence of every channel by itself (swimba_ssd_scan's recurrence with a gate per channel in
+ * place of the head's transition):
+ *   f_t = sigmoid(gate_t),  h_t = f_t h_{t-1} + (1 - f_t) x_t,  h_{-1} = init_state or 0
+ *   x, gate [B][T][W], tokens x_stride and gate_stride apart; init_state [B][W] fp32 or NULL
+ *   h [B][T][W] dtype out; final_state [B][W] fp32 out or NULL (may be init_state)
+ * Where x is not finite, h is not finite from that token until the state is forgotten. */
+swimba_status swimba_gated_scan(const swimba_gated_dims* dims, const void* x, const void* gate, const float* init_state,
+                                void* h, float* final_state, void* stream);
+
+/* Gradients of swimba_gated_scan for L = sum <dh_t, h_t> + <d_final, final_state>, at the stored h:
+ *   x, gate, init_state as given to the forward, h [B][T][W] dtype as it wrote it
+ *   dh [B][T][W] grad_dtype; d_final [B][W] fp32 or NULL
+ *   dx, dgate [B][T][W] grad_dtype out (dense); d_init [B][W] fp32 out or NULL */
+swimba_status swimba_gated_scan_bwd(const swimba_gated_dims* dims, const void* x, const void* gate, const void* h,
+                                    const float* init_state, const void* dh, const float* d_final, void* dx,
+                                    void* dgate, float* d_init, void* stream);
+
+/* One token of swimba_gated_scan for every sequence (dims.seqlen must be 1):
+ *   x, gate [B][W]; state [B][W] fp32, updated in place; h [B][W] dtype out */
+swimba_status swimba_gated_step(const swimba_gated_dims* dims, const void* x, const void* gate, float* state, void* h,
+                                void* stream);
+
+typedef enum { SWIMBA_SILU = 0, SWIMBA_GELU = 1 } swimba_activation; /* GELU: the form with erf */
+
+typedef struct {
+  int32_t rows;       /* M: tokens */
+  int32_t d_model;    /* D */
+  int32_t d_ff;       /* F */
+  int32_t dtype;      /* every tensor's */
+  int32_t activation; /* swimba_activation */
+} swimba_ffn_dims;
+
+/* Bytes of workspace of the two entry points below (0 if the dims are invalid or unsupported).  D and F must be
+ * multiples of 8 (of 4 in fp32). */
+size_t swimba_gated_ffn_workspace_size(const swimba_ffn_dims* dims);
+size_t swimba_gated_ffn_bwd_workspace_size(const swimba_ffn_dims* dims);
+
+/* The gated feed-forward block:
+ *   gate = x W_gate^T,  up = x W_up^T,  h = act(gate) * up,  out = h W_down^T
+ *   x [M][D]; w_gate, w_up [F][D]; w_down [D][F]
+ *   gate, up [M][F] out, each or NULL (kept for the gradients); h [M][F] out; out [M][D] out
+ * Products accumulate in fp32; h is formed from the fp32 values and rounded once, and the last product reads the
+ * rounded h. */
+swimba_status swimba_gated_ffn(const swimba_ffn_dims* dims, const void* x, const void* w_gate, const void* w_up,
+                               const void* w_down, void* gate, void* up, void* h, void* out, void* ws, size_t ws_bytes,
+                               void* stream);
+
+/* Gradients of swimba_gated_ffn for L = sum <dout, out>, at the stored gate, up and h:
+ *   dh = dout W_down,  dgate = dh up act'(gate),  dup = dh act(gate)
+ *   dx [M][D] = dgate W_gate + dup W_up,  dw_gate [F][D] = dgate^T x,  dw_up [F][D] = dup^T x,
+ *   dw_down [D][F] = dout^T h                                                  (all dtype, all out)
+ * dgate and dup are formed from the fp32 dh and rounded once to dtype between the products. */
+swimba_status swimba_gated_ffn_bwd(const swimba_ffn_dims* dims, const void* x, const void* gate, const void* up,
+                                   const void* h, const void* w_gate, const void* w_up, const void* w_down,
+                                   const void* dout, void* dx, void* dw_gate, void* dw_up, void* dw_down, void* ws,
+                                   size_t ws_bytes, void* stream);
+
 /* Synchronises `stream`, then reads and clears the current device's status word: SWIMBA_OK,
  * SWIMBA_ERR_TIMEOUT, SWIMBA_ERR_RANGE, SWIMBA_ERR_INDEX or SWIMBA_ERR_UNSTABLE, in that order of
  * precedence (SWIMBA_ERR_CUDA if the stream reports an error).  The word is sticky: it collects every flag raised on this device

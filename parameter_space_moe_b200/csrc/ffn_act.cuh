@@ -1,0 +1,26 @@
+// Activations of the gated feed-forward block and their slopes, in fp32.  Internal to libswimba.
+//   silu(g) = g s, slope s (1 + g (1 - s)) with s = sigmoid(g);  gelu(g) = g c, slope c + g n with c and n the
+//   normal distribution's cumulative and density at g.
+#pragma once
+#include "block_common.cuh"
+
+namespace swimba {
+
+__device__ __forceinline__ float act_both(float g, int act, float& slope) {
+  if (act == SWIMBA_SILU) {
+    float s, q;
+    gate_pair(g, s, q);
+    slope = s * fmaf(g, q, 1.f);
+    return g * s;
+  }
+  const float c = 0.5f * (1.f + erff(g * 0.70710678f));
+  slope = fmaf(g, 0.39894228f * __expf(-0.5f * g * g), c);
+  return g * c;
+}
+
+__device__ __forceinline__ float act_value(float g, int act) {
+  float slope;
+  return act_both(g, act, slope);
+}
+
+}  // namespace swimba

@@ -5,7 +5,7 @@
 #include <map>
 #include <mutex>
 
-#include "common.cuh"
+#include "block_common.cuh"
 
 namespace swimba {
 
@@ -546,6 +546,167 @@ swimba_status swimba_out_proj(const swimba_dims* dims, const void* y, const void
   unsigned* st = device_status();
   if (!st) return SWIMBA_ERR_CUDA;
   return cuda_status(launch_out_proj(d, y, w_out, out, st, (cudaStream_t)stream));
+}
+
+// ---------------------------------------------------------------------------------------------
+// Operators around the token mixer: dims of their own, the same order of checks.
+static bool any_dtype(int t) { return t == SWIMBA_F32 || t == SWIMBA_BF16 || t == SWIMBA_F16; }
+static bool ok_grad(int g, int t) { return g == SWIMBA_F32 || g == t; }
+
+static swimba_status make_norm_dims(const swimba_norm_dims* in, NormDims* d) {
+  if (!in || in->rows < 1 || in->width < 1 || !any_dtype(in->dtype) || !ok_grad(in->grad_dtype, in->dtype) ||
+      !(in->eps > 0.f) || in->eps > 3.4e38f || (in->x_stride != 0 && in->x_stride < in->width))
+    return SWIMBA_ERR_INVALID_ARG;
+  if (in->width > 16384 || in->x_stride >= (1LL << 31)) return SWIMBA_ERR_UNSUPPORTED;
+  *d = {in->rows, in->width, in->dtype, in->grad_dtype, in->x_stride ? in->x_stride : in->width, in->eps};
+  return SWIMBA_OK;
+}
+
+static swimba_status make_gated_dims(const swimba_gated_dims* in, GatedDims* d) {
+  if (!in || in->batch < 1 || in->seqlen < 1 || in->width < 1 || !any_dtype(in->dtype) ||
+      !ok_grad(in->grad_dtype, in->dtype) || (in->x_stride != 0 && in->x_stride < in->width) ||
+      (in->gate_stride != 0 && in->gate_stride < in->width))
+    return SWIMBA_ERR_INVALID_ARG;
+  // token indexes and the scan's grid (8 CTAs for every 32 channels at most) stay within 31 bits
+  if ((long long)in->batch * in->seqlen >= (1LL << 30) || (long long)in->batch * (in->width / 32 + 1) >= (1LL << 27) ||
+      in->seqlen > (1 << 29) || in->x_stride >= (1LL << 31) || in->gate_stride >= (1LL << 31))
+    return SWIMBA_ERR_UNSUPPORTED;
+  *d = {in->batch, in->seqlen, in->width, in->dtype, in->grad_dtype, in->x_stride ? in->x_stride : in->width,
+        in->gate_stride ? in->gate_stride : in->width};
+  return SWIMBA_OK;
+}
+
+static swimba_status make_ffn_dims(const swimba_ffn_dims* in, FfnDims* d) {
+  if (!in || in->rows < 1 || in->d_model < 1 || in->d_ff < 1 || !any_dtype(in->dtype) ||
+      (in->activation != SWIMBA_SILU && in->activation != SWIMBA_GELU))
+    return SWIMBA_ERR_INVALID_ARG;
+  const int q = in->dtype == SWIMBA_F32 ? 4 : 8;
+  if (in->d_model % q != 0 || in->d_ff % q != 0 || in->d_model > (1 << 20) || in->d_ff > (1 << 20) ||
+      in->rows > (1 << 24))
+    return SWIMBA_ERR_UNSUPPORTED;
+  *d = {in->rows, in->d_model, in->d_ff, in->dtype, in->activation};
+  return SWIMBA_OK;
+}
+
+swimba_status swimba_layer_norm(const swimba_norm_dims* dims, const void* x, const void* residual, const float* gamma,
+                                const float* beta, void* y, void* r_out, void* stream) {
+  NormDims d;
+  SW_TRY(make_norm_dims(dims, &d));
+  if (!ok_ptr(x) || !ok_opt(residual) || !ok_opt(gamma) || !ok_opt(beta) || !ok_ptr(y) || !ok_opt(r_out))
+    return SWIMBA_ERR_INVALID_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  prof_begin(s);
+  SW_CUDA(launch_layer_norm(d, x, residual, gamma, beta, y, r_out, s));
+  prof_mark(s, "layer_norm");
+  return SWIMBA_OK;
+}
+
+size_t swimba_layer_norm_bwd_workspace_size(const swimba_norm_dims* dims) {
+  NormDims d;
+  return make_norm_dims(dims, &d) == SWIMBA_OK ? layer_norm_bwd_ws(d) : 0;
+}
+
+swimba_status swimba_layer_norm_bwd(const swimba_norm_dims* dims, const void* r, const float* gamma, const void* dy,
+                                    const void* dr, void* dx, float* dgamma, float* dbeta, void* ws, size_t ws_bytes,
+                                    void* stream) {
+  NormDims d;
+  SW_TRY(make_norm_dims(dims, &d));
+  if (!ok_ptr(r) || !ok_opt(gamma) || !ok_ptr(dy) || !ok_opt(dr) || !ok_ptr(dx) || !ok_opt(dgamma) || !ok_opt(dbeta))
+    return SWIMBA_ERR_INVALID_ARG;
+  if (!ok_ptr(ws) || ws_bytes < layer_norm_bwd_ws(d)) return SWIMBA_ERR_WORKSPACE;
+  cudaStream_t s = (cudaStream_t)stream;
+  prof_begin(s);
+  SW_CUDA(launch_layer_norm_bwd(d, r, gamma, dy, dr, dx, dgamma, dbeta, (float*)ws, s));
+  prof_mark(s, "layer_norm_bwd");
+  return SWIMBA_OK;
+}
+
+swimba_status swimba_gated_scan(const swimba_gated_dims* dims, const void* x, const void* gate, const float* init_state,
+                                void* h, float* final_state, void* stream) {
+  GatedDims d;
+  SW_TRY(make_gated_dims(dims, &d));
+  if (!ok_ptr(x) || !ok_ptr(gate) || !ok_opt(init_state) || !ok_ptr(h) || !ok_opt(final_state))
+    return SWIMBA_ERR_INVALID_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  prof_begin(s);
+  SW_CUDA(launch_gated_scan(d, x, gate, init_state, h, final_state, s));
+  prof_mark(s, "gated_scan");
+  return SWIMBA_OK;
+}
+
+swimba_status swimba_gated_scan_bwd(const swimba_gated_dims* dims, const void* x, const void* gate, const void* h,
+                                    const float* init_state, const void* dh, const float* d_final, void* dx,
+                                    void* dgate, float* d_init, void* stream) {
+  GatedDims d;
+  SW_TRY(make_gated_dims(dims, &d));
+  if (!ok_ptr(x) || !ok_ptr(gate) || !ok_ptr(h) || !ok_opt(init_state) || !ok_ptr(dh) || !ok_opt(d_final) ||
+      !ok_ptr(dx) || !ok_ptr(dgate) || !ok_opt(d_init))
+    return SWIMBA_ERR_INVALID_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  prof_begin(s);
+  SW_CUDA(launch_gated_scan_bwd(d, x, gate, h, init_state, dh, d_final, dx, dgate, d_init, s));
+  prof_mark(s, "gated_scan_bwd");
+  return SWIMBA_OK;
+}
+
+swimba_status swimba_gated_step(const swimba_gated_dims* dims, const void* x, const void* gate, float* state, void* h,
+                                void* stream) {
+  GatedDims d;
+  SW_TRY(make_gated_dims(dims, &d));
+  if (d.T != 1 || !ok_ptr(x) || !ok_ptr(gate) || !ok_ptr(state) || !ok_ptr(h)) return SWIMBA_ERR_INVALID_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  prof_begin(s);
+  SW_CUDA(launch_gated_step(d, x, gate, state, h, s));
+  prof_mark(s, "gated_step");
+  return SWIMBA_OK;
+}
+
+size_t swimba_gated_ffn_workspace_size(const swimba_ffn_dims* dims) {
+  FfnDims d;
+  return make_ffn_dims(dims, &d) == SWIMBA_OK ? gated_ffn_ws(d) : 0;
+}
+
+size_t swimba_gated_ffn_bwd_workspace_size(const swimba_ffn_dims* dims) {
+  FfnDims d;
+  return make_ffn_dims(dims, &d) == SWIMBA_OK ? gated_ffn_bwd_ws(d) : 0;
+}
+
+swimba_status swimba_gated_ffn(const swimba_ffn_dims* dims, const void* x, const void* w_gate, const void* w_up,
+                               const void* w_down, void* gate, void* up, void* h, void* out, void* ws, size_t ws_bytes,
+                               void* stream) {
+  FfnDims d;
+  SW_TRY(make_ffn_dims(dims, &d));
+  if (!ok_ptr(x) || !ok_ptr(w_gate) || !ok_ptr(w_up) || !ok_ptr(w_down) || !ok_opt(gate) || !ok_opt(up) || !ok_ptr(h) ||
+      !ok_ptr(out))
+    return SWIMBA_ERR_INVALID_ARG;
+  if (!ok_ptr(ws) || ws_bytes < gated_ffn_ws(d)) return SWIMBA_ERR_WORKSPACE;
+  unsigned* st = device_status();
+  if (!st) return SWIMBA_ERR_CUDA;
+  cudaStream_t s = (cudaStream_t)stream;
+  prof_begin(s);
+  SW_CUDA(launch_gated_ffn(d, x, w_gate, w_up, w_down, gate, up, h, out, (char*)ws, st, s));
+  prof_mark(s, "gated_ffn");
+  return SWIMBA_OK;
+}
+
+swimba_status swimba_gated_ffn_bwd(const swimba_ffn_dims* dims, const void* x, const void* gate, const void* up,
+                                   const void* h, const void* w_gate, const void* w_up, const void* w_down,
+                                   const void* dout, void* dx, void* dw_gate, void* dw_up, void* dw_down, void* ws,
+                                   size_t ws_bytes, void* stream) {
+  FfnDims d;
+  SW_TRY(make_ffn_dims(dims, &d));
+  if (!ok_ptr(x) || !ok_ptr(gate) || !ok_ptr(up) || !ok_ptr(h) || !ok_ptr(w_gate) || !ok_ptr(w_up) || !ok_ptr(w_down) ||
+      !ok_ptr(dout) || !ok_ptr(dx) || !ok_ptr(dw_gate) || !ok_ptr(dw_up) || !ok_ptr(dw_down))
+    return SWIMBA_ERR_INVALID_ARG;
+  if (!ok_ptr(ws) || ws_bytes < gated_ffn_bwd_ws(d)) return SWIMBA_ERR_WORKSPACE;
+  unsigned* st = device_status();
+  if (!st) return SWIMBA_ERR_CUDA;
+  cudaStream_t s = (cudaStream_t)stream;
+  prof_begin(s);
+  SW_CUDA(launch_gated_ffn_bwd(d, x, gate, up, h, w_gate, w_up, w_down, dout, dx, dw_gate, dw_up, dw_down, (char*)ws,
+                               st, s));
+  prof_mark(s, "gated_ffn_bwd");
+  return SWIMBA_OK;
 }
 
 // Workspace of swimba_layer_bwd: the layer's own, then the gradient buffers (all fp32).

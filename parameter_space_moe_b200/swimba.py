@@ -15,6 +15,7 @@ LIB_PATH = os.path.join(_HERE, "libswimba.so")
 
 F32, BF16, F16 = 0, 1, 2
 MIX_UNSCALED_B = 1
+SILU, GELU = 0, 1
 STATUS = {0: "SWIMBA_OK", 1: "SWIMBA_ERR_INVALID_ARG", 2: "SWIMBA_ERR_UNSUPPORTED", 3: "SWIMBA_ERR_CUDA",
           4: "SWIMBA_ERR_WORKSPACE", 5: "SWIMBA_ERR_TIMEOUT", 6: "SWIMBA_ERR_RANGE", 7: "SWIMBA_ERR_INDEX",
           8: "SWIMBA_ERR_UNSTABLE"}
@@ -23,7 +24,10 @@ EXPORTS = ("swimba_workspace_size", "swimba_stream_dtype", "swimba_router_topk",
            "swimba_separated_scan", "swimba_check_device_status", "swimba_status_string",
            "swimba_profile_enable", "swimba_profile_read", "swimba_launch_count", "swimba_dispatch_noalloc",
            "swimba_layer_fwd_host", "swimba_debug_scan_lost_first_chunk", "swimba_out_proj",
-           "swimba_ssd_scan_bwd", "swimba_layer_bwd", "swimba_layer_bwd_workspace_size")
+           "swimba_ssd_scan_bwd", "swimba_layer_bwd", "swimba_layer_bwd_workspace_size", "swimba_layer_norm",
+           "swimba_layer_norm_bwd", "swimba_layer_norm_bwd_workspace_size", "swimba_gated_scan",
+           "swimba_gated_scan_bwd", "swimba_gated_step", "swimba_gated_ffn", "swimba_gated_ffn_bwd",
+           "swimba_gated_ffn_workspace_size", "swimba_gated_ffn_bwd_workspace_size")
 
 
 class SwimbaError(RuntimeError):
@@ -40,6 +44,21 @@ class Dims(ctypes.Structure):
 class Weights(ctypes.Structure):
     _fields_ = [("w_router", ctypes.c_void_p), ("w_dt", ctypes.c_void_p), ("b_dt", ctypes.c_void_p),
                 ("A", ctypes.c_void_p), ("w_exp", ctypes.c_void_p), ("A_exp", ctypes.c_void_p)]
+
+
+class NormDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("width", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("x_stride", ctypes.c_int64), ("eps", ctypes.c_float)]
+
+
+class GatedDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("seqlen", ctypes.c_int32), ("width", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("x_stride", ctypes.c_int64),
+                ("gate_stride", ctypes.c_int64)]
+
+
+class FfnDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "d_model", "d_ff", "dtype", "activation")]
 
 
 _lib = None
@@ -60,6 +79,10 @@ def lib():
         L.swimba_stream_dtype.argtypes = [P(Dims)]
         L.swimba_layer_bwd_workspace_size.restype = sz
         L.swimba_layer_bwd_workspace_size.argtypes = [P(Dims)]
+        for name, t in (("layer_norm_bwd", NormDims), ("gated_ffn", FfnDims), ("gated_ffn_bwd", FfnDims)):
+            f = getattr(L, f"swimba_{name}_workspace_size")
+            f.restype = sz
+            f.argtypes = [P(t)]
         L.swimba_status_string.restype = ctypes.c_char_p
         L.swimba_status_string.argtypes = [ctypes.c_int]
         sig = {
@@ -78,6 +101,13 @@ def lib():
             "swimba_ssd_scan_bwd": [P(Dims), vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
             "swimba_layer_bwd": [P(Dims), vp, P(Weights), vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
             "swimba_check_device_status": [vp],
+            "swimba_layer_norm": [P(NormDims)] + [vp] * 7,
+            "swimba_layer_norm_bwd": [P(NormDims)] + [vp] * 8 + [sz, vp],
+            "swimba_gated_scan": [P(GatedDims)] + [vp] * 6,
+            "swimba_gated_scan_bwd": [P(GatedDims)] + [vp] * 10,
+            "swimba_gated_step": [P(GatedDims)] + [vp] * 5,
+            "swimba_gated_ffn": [P(FfnDims)] + [vp] * 9 + [sz, vp],
+            "swimba_gated_ffn_bwd": [P(FfnDims)] + [vp] * 13 + [sz, vp],
         }
         L.swimba_profile_enable.restype = ctypes.c_int
         L.swimba_profile_enable.argtypes = [ctypes.c_int]
@@ -211,6 +241,170 @@ def layer_bwd(d, X, W, init_state, dy, dX, dW_r, dW_dt, db_dt, dA, dW_exp, d_ini
 
 def out_proj(d, y, w_out, out, stream=None):
     _check("swimba_out_proj", lib().swimba_out_proj(ctypes.byref(d), _p(y), _p(w_out), _p(out), _stream(stream)))
+
+
+# ------------------------------------------------------------------ operators around the token mixer
+# These check what they are given (SwimbaError with SWIMBA_ERR_INVALID_ARG): every tensor of the dims' dtype and
+# size, on one GPU, dense (x and gate: dense but for their row stride).  They run on that GPU's current stream
+# unless one is given.
+
+_TORCH = {F32: torch.float32, BF16: torch.bfloat16, F16: torch.float16}
+_NBYTES = {F32: 4, BF16: 2, F16: 2}
+
+
+def norm_dims(rows, width, dtype, grad_dtype=None, x_stride=0, eps=1e-5):
+    return NormDims(rows, width, dtype, dtype if grad_dtype is None else grad_dtype, x_stride, eps)
+
+
+def gated_dims(batch, seqlen, width, dtype, grad_dtype=None, x_stride=0, gate_stride=0):
+    return GatedDims(batch, seqlen, width, dtype, dtype if grad_dtype is None else grad_dtype, x_stride, gate_stride)
+
+
+def ffn_dims(rows, d_model, d_ff, dtype, activation=SILU):
+    return FfnDims(rows, d_model, d_ff, dtype, activation)
+
+
+def _dense(fn, dev, n, dtype, *tensors):
+    """Pointers of dense tensors of n elements of one dtype on GPU `dev` (None passes)."""
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if t.get_device() != dev or t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+            raise SwimbaError(fn, 1)
+        out.append(t.data_ptr())
+    return out
+
+
+def _rows(fn, dev, rows, width, stride, dtype, t):
+    """Pointer of a tensor of rows x width whose rows (all leading dimensions flattened) lie `stride` apart."""
+    if t.get_device() != dev or t.dtype is not dtype or t.numel() != rows * width or t.shape[-1] != width:
+        raise SwimbaError(fn, 1)
+    if not t.is_contiguous() or (stride and stride != width and rows > 1):
+        step, shape = stride or width, t.shape
+        if width > 1 and t.stride(-1) != 1:
+            raise SwimbaError(fn, 1)
+        for k in range(len(shape) - 2, -1, -1):
+            if shape[k] > 1 and t.stride(k) != step:
+                raise SwimbaError(fn, 1)
+            step *= shape[k]
+    return t.data_ptr()
+
+
+def _device(fn, t):
+    dev = t.get_device() if t is not None else -1
+    if dev < 0:
+        raise SwimbaError(fn, 1)
+    return dev
+
+
+def _run(fn, dev, stream, *args):
+    """Calls the library with GPU `dev` current, on its current stream or the given one (of that GPU)."""
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        if stream.device.index != dev:
+            raise SwimbaError(fn, 1)
+        s = stream.cuda_stream
+    call = getattr(_lib or lib(), fn)
+    if dev == torch.cuda.current_device():
+        code = call(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            code = call(*args, s)
+    if code:
+        raise SwimbaError(fn, code)
+
+
+def layer_norm(d, x, residual, gamma, beta, y, r_out, stream=None):
+    fn, dev = "swimba_layer_norm", _device("swimba_layer_norm", x)
+    T, n = _TORCH.get(d.dtype), d.rows * d.width
+    px = _rows(fn, dev, d.rows, d.width, d.x_stride, T, x)
+    res, py, pr = _dense(fn, dev, n, T, residual, y, r_out)
+    pg, pb = _dense(fn, dev, d.width, torch.float32, gamma, beta)
+    _run(fn, dev, stream, d, px, res, pg, pb, py, pr)
+
+
+def layer_norm_bwd_workspace_size(d):
+    return lib().swimba_layer_norm_bwd_workspace_size(d)
+
+
+def layer_norm_bwd(d, r, gamma, dy, dr, dx, dgamma, dbeta, ws, stream=None):
+    fn, dev = "swimba_layer_norm_bwd", _device("swimba_layer_norm_bwd", r)
+    n = d.rows * d.width
+    pr, = _dense(fn, dev, n, _TORCH.get(d.dtype), r)
+    pdy, pdr, pdx = _dense(fn, dev, n, _TORCH.get(d.grad_dtype), dy, dr, dx)
+    pg, pdg, pdb = _dense(fn, dev, d.width, torch.float32, gamma, dgamma, dbeta)
+    pws, nws = _workspace(fn, dev, ws)
+    _run(fn, dev, stream, d, pr, pg, pdy, pdr, pdx, pdg, pdb, pws, nws)
+
+
+def _workspace(fn, dev, ws):
+    if ws is None:
+        return None, 0
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise SwimbaError(fn, 1)
+    return ws.data_ptr(), ws.nbytes
+
+
+def gated_scan(d, x, gate, init_state, h, final_state, stream=None):
+    fn, dev = "swimba_gated_scan", _device("swimba_gated_scan", x)
+    T, m, W = _TORCH.get(d.dtype), d.batch * d.seqlen, d.width
+    px = _rows(fn, dev, m, W, d.x_stride, T, x)
+    pg = _rows(fn, dev, m, W, d.gate_stride, T, gate)
+    ph, = _dense(fn, dev, m * W, T, h)
+    p0, p1 = _dense(fn, dev, d.batch * W, torch.float32, init_state, final_state)
+    _run(fn, dev, stream, d, px, pg, p0, ph, p1)
+
+
+def gated_scan_bwd(d, x, gate, h, init_state, dh, d_final, dx, dgate, d_init, stream=None):
+    fn, dev = "swimba_gated_scan_bwd", _device("swimba_gated_scan_bwd", x)
+    T, m, W = _TORCH.get(d.dtype), d.batch * d.seqlen, d.width
+    px = _rows(fn, dev, m, W, d.x_stride, T, x)
+    pg = _rows(fn, dev, m, W, d.gate_stride, T, gate)
+    ph, = _dense(fn, dev, m * W, T, h)
+    pdh, pdx, pdg = _dense(fn, dev, m * W, _TORCH.get(d.grad_dtype), dh, dx, dgate)
+    p0, p1, p2 = _dense(fn, dev, d.batch * W, torch.float32, init_state, d_final, d_init)
+    _run(fn, dev, stream, d, px, pg, ph, p0, pdh, p1, pdx, pdg, p2)
+
+
+def gated_step(d, x, gate, state, h, stream=None):
+    fn, dev = "swimba_gated_step", _device("swimba_gated_step", x)
+    T, m, W = _TORCH.get(d.dtype), d.batch * d.seqlen, d.width
+    px = _rows(fn, dev, m, W, d.x_stride, T, x)
+    pg = _rows(fn, dev, m, W, d.gate_stride, T, gate)
+    ph, = _dense(fn, dev, m * W, T, h)
+    ps, = _dense(fn, dev, m * W, torch.float32, state)
+    _run(fn, dev, stream, d, px, pg, ps, ph)
+
+
+def gated_ffn_workspace_size(d):
+    return lib().swimba_gated_ffn_workspace_size(d)
+
+
+def gated_ffn_bwd_workspace_size(d):
+    return lib().swimba_gated_ffn_bwd_workspace_size(d)
+
+
+def gated_ffn(d, x, w_gate, w_up, w_down, gate, up, h, out, ws, stream=None):
+    fn, dev = "swimba_gated_ffn", _device("swimba_gated_ffn", x)
+    T = _TORCH.get(d.dtype)
+    px, po = _dense(fn, dev, d.rows * d.d_model, T, x, out)
+    wg, wu, wd = _dense(fn, dev, d.d_ff * d.d_model, T, w_gate, w_up, w_down)
+    pg, pu, ph = _dense(fn, dev, d.rows * d.d_ff, T, gate, up, h)
+    pws, nws = _workspace(fn, dev, ws)
+    _run(fn, dev, stream, d, px, wg, wu, wd, pg, pu, ph, po, pws, nws)
+
+
+def gated_ffn_bwd(d, x, gate, up, h, w_gate, w_up, w_down, dout, dx, dw_gate, dw_up, dw_down, ws, stream=None):
+    fn, dev = "swimba_gated_ffn_bwd", _device("swimba_gated_ffn_bwd", x)
+    T = _TORCH.get(d.dtype)
+    px, pdo, pdx = _dense(fn, dev, d.rows * d.d_model, T, x, dout, dx)
+    wg, wu, wd, dg, du, dd = _dense(fn, dev, d.d_ff * d.d_model, T, w_gate, w_up, w_down, dw_gate, dw_up, dw_down)
+    pg, pu, ph = _dense(fn, dev, d.rows * d.d_ff, T, gate, up, h)
+    pws, nws = _workspace(fn, dev, ws)
+    _run(fn, dev, stream, d, px, pg, pu, ph, wg, wu, wd, pdo, pdx, dg, du, dd, pws, nws)
 
 
 def debug_scan_lost_first_chunk(d, Bpi, Xs, Cpi, dt, A, y, ws, stream=None):
