@@ -15,6 +15,7 @@
 
 #include "block_common.cuh"
 #include "ffn_act.cuh"
+#include "ffn_tc.cuh"
 
 namespace swimba {
 
@@ -200,30 +201,106 @@ cudaError_t bwd_t(const FfnDims& d, const T* x, const T* gate, const T* up, cons
 
 }  // namespace
 
-size_t gated_ffn_ws(const FfnDims& d) { return 256; }
+namespace {
+
+// The tensor-core launches of the block: operands by number, one problem per product.
+FfnProblem problem(int M, int N, int K, int a, bool a_mn, int b, bool b_mn, void* out) {
+  FfnProblem q{};
+  q.M = M; q.N = N; q.K = K; q.a_mn = a_mn; q.b_mn = b_mn; q.nseg = 1;
+  q.a[0] = (unsigned char)a; q.b[0] = (unsigned char)b;
+  q.out = out;
+  return q;
+}
+
+FfnLaunch launch_of(const FfnDims& d, int epi, int nop) {
+  FfnLaunch l{};
+  l.epi = epi; l.act = d.act; l.dtype = l.op_dtype = d.dtype; l.nop = nop;
+  return l;
+}
+
+// h (and gate and up) = x, the two weights.
+FfnLaunch glu_launch(const FfnDims& d, const void* x, const void* wg, const void* wu, void* gate, void* up, void* h) {
+  FfnLaunch l = launch_of(d, kFfnGlu, 3);
+  l.op[0] = {x, d.M, d.D, 1}; l.op[1] = {wg, d.F, d.D, 1}; l.op[2] = {wu, d.F, d.D, 1};
+  l.nprob = 1;
+  l.prob[0] = problem(d.M, d.F, d.D, 0, false, 1, false, h);
+  l.prob[0].b_up = 2;
+  l.out2 = gate; l.out3 = up;
+  return l;
+}
+
+FfnLaunch down_launch(const FfnDims& d, const void* h, const void* wd, void* out) {
+  FfnLaunch l = launch_of(d, kFfnStore, 2);
+  l.op[0] = {h, d.M, d.F, 1}; l.op[1] = {wd, d.D, d.F, 1};
+  l.nprob = 1;
+  l.prob[0] = problem(d.M, d.D, d.F, 0, false, 1, false, out);
+  return l;
+}
+
+FfnLaunch dglu_launch(const FfnDims& d, const void* dout, const void* wd, const void* gate, const void* up, void* dgate,
+                      void* dup) {
+  FfnLaunch l = launch_of(d, kFfnDglu, 2);
+  l.op[0] = {dout, d.M, d.D, 1}; l.op[1] = {wd, d.D, d.F, 1};
+  l.nprob = 1;
+  l.prob[0] = problem(d.M, d.F, d.D, 0, false, 1, true, dgate);
+  l.out2 = dup; l.in1 = gate; l.in2 = up;
+  return l;
+}
+
+// dx (K = both halves of the features) and the three weight gradients (K = the tokens) in one launch.
+FfnLaunch grads_launch(const FfnDims& d, const void* x, const void* h, const void* wg, const void* wu, const void* dout,
+                       const void* dgate, const void* dup, void* dx, void* dwg, void* dwu, void* dwd) {
+  FfnLaunch l = launch_of(d, kFfnStore, 7);
+  l.op[0] = {dgate, d.M, d.F, 1}; l.op[1] = {dup, d.M, d.F, 1}; l.op[2] = {wg, d.F, d.D, 1}; l.op[3] = {wu, d.F, d.D, 1};
+  l.op[4] = {x, d.M, d.D, 1}; l.op[5] = {dout, d.M, d.D, 1}; l.op[6] = {h, d.M, d.F, 1};
+  l.nprob = 4;
+  l.prob[0] = problem(d.M, d.D, d.F, 0, false, 2, true, dx);
+  l.prob[0].nseg = 2; l.prob[0].a[1] = 1; l.prob[0].b[1] = 3;
+  l.prob[1] = problem(d.F, d.D, d.M, 0, true, 4, true, dwg);
+  l.prob[2] = problem(d.F, d.D, d.M, 1, true, 4, true, dwu);
+  l.prob[3] = problem(d.D, d.F, d.M, 5, true, 6, true, dwd);
+  return l;
+}
+
+bool tensor_cores(const FfnDims& d) { return d.dtype != SWIMBA_F32; }
+size_t half_bytes(const FfnDims& d) { return align_up((size_t)d.M * d.F * elem_bytes(d.dtype), 256); }
+
+}  // namespace
+
+size_t gated_ffn_ws(const FfnDims& d) {
+  return 256 + (tensor_cores(d) ? ffn_tc_partial_bytes(down_launch(d, nullptr, nullptr, nullptr)) : 0);
+}
 size_t gated_ffn_bwd_ws(const FfnDims& d) {
-  return 2 * align_up((size_t)d.M * d.F * elem_bytes(d.dtype), 256);
+  size_t n = 2 * half_bytes(d);
+  if (tensor_cores(d))
+    n += ffn_tc_partial_bytes(grads_launch(d, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr,
+                                           nullptr, nullptr, nullptr));
+  return n;
 }
 
 cudaError_t launch_gated_ffn(const FfnDims& d, const void* x, const void* wg, const void* wu, const void* wd, void* gate,
                              void* up, void* h, void* out, char* ws, unsigned* st, cudaStream_t s) {
-  auto go = [&](auto t) {
-    using T = decltype(t);
-    return fwd_t<T>(d, (const T*)x, (const T*)wg, (const T*)wu, (const T*)wd, (T*)gate, (T*)up, (T*)h, (T*)out, s);
-  };
-  return d.dtype == SWIMBA_F32 ? go(float()) : d.dtype == SWIMBA_BF16 ? go(__nv_bfloat16()) : go(__half());
+  if (tensor_cores(d)) {
+    FFN_TRY(launch_ffn_tc(glu_launch(d, x, wg, wu, gate, up, h), nullptr, st, s));
+    return launch_ffn_tc(down_launch(d, h, wd, out), (float*)ws, st, s);
+  }
+  return fwd_t<float>(d, (const float*)x, (const float*)wg, (const float*)wu, (const float*)wd, (float*)gate, (float*)up,
+                      (float*)h, (float*)out, s);
 }
 
 cudaError_t launch_gated_ffn_bwd(const FfnDims& d, const void* x, const void* gate, const void* up, const void* h,
                                  const void* wg, const void* wu, const void* wd, const void* dout, void* dx, void* dwg,
                                  void* dwu, void* dwd, char* ws, unsigned* st, cudaStream_t s) {
-  char* ws2 = ws + align_up((size_t)d.M * d.F * elem_bytes(d.dtype), 256);
-  auto go = [&](auto t) {
-    using T = decltype(t);
-    return bwd_t<T>(d, (const T*)x, (const T*)gate, (const T*)up, (const T*)h, (const T*)wg, (const T*)wu, (const T*)wd,
-                    (const T*)dout, (T*)dx, (T*)dwg, (T*)dwu, (T*)dwd, (T*)ws, (T*)ws2, s);
-  };
-  return d.dtype == SWIMBA_F32 ? go(float()) : d.dtype == SWIMBA_BF16 ? go(__nv_bfloat16()) : go(__half());
+  char* dgate = ws;
+  char* dup = ws + half_bytes(d);
+  if (tensor_cores(d)) {
+    FFN_TRY(launch_ffn_tc(dglu_launch(d, dout, wd, gate, up, dgate, dup), nullptr, st, s));
+    return launch_ffn_tc(grads_launch(d, x, h, wg, wu, dout, dgate, dup, dx, dwg, dwu, dwd),
+                         (float*)(ws + 2 * half_bytes(d)), st, s);
+  }
+  return bwd_t<float>(d, (const float*)x, (const float*)gate, (const float*)up, (const float*)h, (const float*)wg,
+                      (const float*)wu, (const float*)wd, (const float*)dout, (float*)dx, (float*)dwg, (float*)dwu,
+                      (float*)dwd, (float*)dgate, (float*)dup, s);
 }
 
 }  // namespace swimba

@@ -278,5 +278,8 @@ bool encode_tmap_2d(CUtensorMap* map, const void* base, int dtype, uint64_t cols
 // selects one slot of box_rows consecutive rows.
 bool encode_tmap_3d_slot(CUtensorMap* map, const void* base, int dtype, uint64_t cols, uint64_t slots, uint64_t rows,
                          uint32_t box_cols, uint32_t box_rows);
+// Host: 3D map of [planes][rows][cols] (dims {cols, rows, planes}); box {box_cols, box_rows, 1} in one plane.
+bool encode_tmap_3d_planes(CUtensorMap* map, const void* base, int dtype, uint64_t cols, uint64_t rows, uint64_t planes,
+                           uint32_t box_cols, uint32_t box_rows);
 
 }  // namespace swimba
