@@ -51,12 +51,38 @@ __device__ __forceinline__ void load_vec(const T* p, float (&v)[VEC]) {
   }
 }
 
+// Two values rounded to a 16-bit type by one conversion, a in the lower half.
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+  uint32_t u;
+  memcpy(&u, &r, 4);
+  return u;
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+  const __half2 r = __floats2half2_rn(a, b);
+  uint32_t u;
+  memcpy(&u, &r, 4);
+  return u;
+}
+
 template <class T, int VEC>
 __device__ __forceinline__ void store_vec(T* p, const float (&v)[VEC]) {
   constexpr int kBytes = VEC * (int)sizeof(T);
   T t[VEC];
+  if constexpr (sizeof(T) == 2 && VEC % 2 == 0) {
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) t[j] = from_f32<T>(v[j]);
+    for (int j = 0; j < VEC; j += 2) {
+      const uint32_t u = pack2<T>(v[j], v[j + 1]);
+      memcpy(t + j, &u, 4);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) t[j] = from_f32<T>(v[j]);
+  }
   if constexpr (kBytes % 16 == 0) {
 #pragma unroll
     for (int b = 0; b < kBytes / 16; ++b) {
@@ -78,12 +104,25 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[VEC]) {
   }
 }
 
+// e^x and 1 / x by the hardware's approximations alone (2 ulp and 1 ulp; subnormal results and operands are 0), where
+// __expf and __fdividef add instructions for subnormals.
+__device__ __forceinline__ float exp_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // f = sigmoid(g) and q = sigmoid(-g) = 1 - f.  The smaller of the two comes from exp(-|g|) in (0, 1], the larger as
 // its complement to 1: neither overflows, the small one keeps its relative accuracy, and a gate near 1 is rounded
 // once (a bias there would grow with the length of the memory).
 __device__ __forceinline__ void gate_pair(float g, float& f, float& q) {
-  const float e = __expf(-fabsf(g));
-  const float small = __fdividef(e, 1.f + e), large = 1.f - small;
+  const float e = exp_fast(-fabsf(g));
+  const float small = e * rcp_fast(1.f + e), large = 1.f - small;
   f = g >= 0.f ? large : small;
   q = g >= 0.f ? small : large;
 }

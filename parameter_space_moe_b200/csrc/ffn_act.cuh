@@ -14,13 +14,14 @@ __device__ __forceinline__ float act_both(float g, int act, float& slope) {
     return g * s;
   }
   const float c = 0.5f * (1.f + erff(g * 0.70710678f));
-  slope = fmaf(g, 0.39894228f * __expf(-0.5f * g * g), c);
+  slope = fmaf(g, 0.39894228f * exp_fast(-0.5f * g * g), c);
   return g * c;
 }
 
+// .
 __device__ __forceinline__ float act_value(float g, int act) {
-  float slope;
-  return act_both(g, act, slope);
+  if (act == SWIMBA_SILU) return g * rcp_fast(1.f + exp_fast(-g));
+  return g * (0.5f * (1.f + erff(g * 0.70710678f)));
 }
 
 }  // namespace swimba

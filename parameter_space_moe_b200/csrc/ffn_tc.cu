@@ -1,14 +1,17 @@
 // The products of the gated feed-forward block and of its gradients on the 5th-generation tensor cores, with the
 // activation (or its gradient) in the epilogue: 16-bit operands, fp32 accumulation in TMEM.
 //
-// One kernel serves all of them.  Every operand is fetched in 64 x 64 boxes (128-byte swizzle): as rows of K for
-// an operand stored along K, or as rows of M or N for one stored across, which the MMA then reads MN-major, so no
-// operand is ever transposed in memory and one tensor map per tensor serves every role.
+// One kernel serves all of them.  Every operand is fetched in boxes of 64 columns x 128 rows (128-byte swizzle): two
+// boxes along K for an operand stored along K, two along M or N for one stored across, which the MMA then reads
+// MN-major.  So no operand is ever transposed in memory and one tensor map per tensor serves every role.
 //   tile        256 x 256 by a CTA pair (cta_group::2, M256 N256 K16: each CTA loads 128 rows of A and 128 of B), or
 //               128 x 128 by one CTA where pairs would leave SMs without work
-//   warp 0      TMA producer: A 16 KB + B 16 KB per 64-wide K slice, a ring of kStages
+//   warp 0      TMA producer: A 32 KB + B 32 KB per 128-wide K slice, a ring of kStages
 //   warp 1      TMEM owner and MMA issuer, two accumulators in TMEM
-//   warps 2..9  epilogue from TMEM: a thread holds one row, 32 columns at a time, and stores whole sectors
+//   warps 2..9  epilogue from TMEM: a thread holds one row, 32 columns at a time; each warp stages its 32 x 32 block
+//               in shared memory (64-byte swizzle: no bank conflicts) and stores it with TMA, two blocks in flight.
+//               Stored from registers, a warp's 16-byte stores touched 32 rows each and held the epilogue of the
+//               8192 x 768 x 2048 forward to 10 us a tile, twice the tile's MMAs
 // Persistent over the units (problem, tile, split of K); a product with few tiles is split along K into fp32
 // partial sums, added in a fixed order by a second kernel.
 #include "ffn_act.cuh"
@@ -19,26 +22,37 @@ namespace swimba {
 
 namespace {
 
-constexpr int BK = 64, kStages = 6;
-constexpr int kEpiWarps = 8, kThreads = 64 + 32 * kEpiWarps;
-constexpr uint32_t kBox = 64 * 128;                 // one 64 x 64 box of 16-bit values
+#ifndef KST
+#define KST 3
+#define KBL 2
+#define KEW 8
+#endif
+constexpr int BK = 128, kStages = KST;
+constexpr int kBlocks = KBL;  // staged blocks of an epilogue warp
+constexpr int kPairWarps = KEW, kOneWarps = 8;     // epilogue warps
+constexpr int epi_warps(bool pair) { return pair ? kPairWarps : kOneWarps; }
+constexpr int block_threads(bool pair) { return 64 + 32 * epi_warps(pair); }
+constexpr uint32_t kBox = 64 * 2 * 128;             // 64 columns of 128 rows, 16-bit
 constexpr uint32_t kStageBytes = 4 * kBox;          // two boxes of A, two of B
-constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + 256;
+constexpr uint32_t kBlock = 32 * 64;                // an epilogue warp's staged block: 32 rows of 64 bytes
+constexpr size_t smem_bytes(bool pair) {
+  return 1024 + (size_t)kStages * kStageBytes + epi_warps(pair) * kBlocks * kBlock + 256;
+}
 constexpr int kSms = 148;                           // what the plan fills; the launch asks the device
 constexpr int kMaxSplit = 16;
 
 struct Prob {
   int M, N, kbs, nkb, a_mn, b_mn;  // kbs: K blocks of a segment, nkb: of all
-  unsigned char a[12], a_plane[12], b[12], b_plane[12], b_up;
+  unsigned char a[12], a_plane[12], b[12], b_plane[12], b_up[12];
   int tiles_m, tiles_n, split, begin;  // first unit
-  void* out;
-  float* part;  // [split][M][N] where split > 1
+  int out;      // number of its output's map
+  void* dst;    // the output itself, and
+  float* part;  // its partial sums [split][M][N] where split > 1
 };
 
 struct Args {
   int nprob, units, act, ab_bf16;
-  void* out2;
-  void* out3;
+  int out2, out3;  // numbers of the maps, -1 without
   const void* in1;
   const void* in2;
   unsigned* st;
@@ -47,6 +61,7 @@ struct Args {
 
 struct Maps {
   CUtensorMap m[kFfnMaxOperands];
+  CUtensorMap o[kFfnMaxProblems + 2];
 };
 
 struct Unit {
@@ -84,30 +99,54 @@ __device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, uint
         : "memory");
 }
 
-// 32 columns of one row, those below n - c0 of them (n - c0 is a multiple of 8, of 4 in fp32).
+// Stores a warp's 32 x 32 block, lane i holding row i, at (row m, column n, plane) of the output behind `map`.  The
+// warp's two staging blocks are used in turn; `lane` 0 owns the copies.
 template <class T>
-__device__ __forceinline__ void store_row(T* p, const float (&v)[32], int left) {
-  constexpr int V = 16 / (int)sizeof(T);
+__device__ __forceinline__ void store_block(const CUtensorMap* map, uint8_t* stage, int& turn, int lane, const float (&v)[32],
+                                            int n, int m, int plane) {
+  constexpr int kCols = 64 / (int)sizeof(T);
 #pragma unroll
-  for (int i = 0; i < 32 / V; ++i)
-    if (i * V < left) {
-      float w[V];
+  for (int h = 0; h < 32 / kCols; ++h) {
+    uint8_t* b = stage + turn * kBlock;
+    turn = turn + 1 == kBlocks ? 0 : turn + 1;
+    if (lane == 0) tc::bulk_wait_read<kBlocks - 1>();  // this block's last copy has read it
+    __syncwarp();
 #pragma unroll
-      for (int j = 0; j < V; ++j) w[j] = v[i * V + j];
-      store_vec<T, V>(p + i * V, w);
+    for (int c = 0; c < 4; ++c) {
+      float w[kCols / 4];
+#pragma unroll
+      for (int j = 0; j < kCols / 4; ++j) w[j] = v[h * kCols + c * (kCols / 4) + j];
+      store_vec<T, kCols / 4>(reinterpret_cast<T*>(b + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)), w);
     }
+    tc::fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) {
+      tc::tma_store_3d(map, b, n + h * kCols, m, plane);
+      tc::bulk_commit();
+    }
+  }
+}
+
+// The 32 values at p as four vectors; those from `left` on (a multiple of 8), or all of a dead row, are 0.
+template <class T>
+__device__ __forceinline__ void load_row(const T* p, bool live, int left, uint4 (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = live && 8 * i < left ? reinterpret_cast<const uint4*>(p)[i] : make_uint4(0u, 0u, 0u, 0u);
 }
 
 template <bool kPair, int kEpi, class T>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(block_threads(kPair), 1)
 ffn_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a) {
   constexpr int TM = kPair ? 256 : 128, TN = kPair ? 256 : 128;
   constexpr int kFeat = kEpi == kFfnGlu ? TN / 2 : TN;  // output columns of a tile
   constexpr uint32_t kTmemCols = 2 * TN;
+  constexpr int kEpiWarps = epi_warps(kPair);
+  constexpr int kPart = kFeat / (kEpiWarps / 4);        // columns of a tile that one warp drains
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = tc::smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes + kEpiWarps * kBlocks * kBlock);
   uint64_t* full = bars;
   uint64_t* empty = bars + kStages;
   uint64_t* acc_full = bars + 2 * kStages;
@@ -168,22 +207,27 @@ ffn_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
         const CUtensorMap* ma = &maps.m[q.a[seg]];
         const CUtensorMap* mb = &maps.m[q.b[seg]];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int m = m0 + 64 * j;
-          load_box<kPair>(sa + j * kBox, ma, fb, q.a_mn ? m : k, q.a_mn ? k : m, q.a_plane[seg]);
-        }
+        for (int j = 0; j < 2; ++j)
+          load_box<kPair>(sa + j * kBox, ma, fb, q.a_mn ? m0 + 64 * j : k + 64 * j, q.a_mn ? k : m0, q.a_plane[seg]);
+        uint8_t* sb = sa + 2 * kBox;
+        if (kEpi == kFfnGlu) {
+          // the first half of the tile's columns are gate rows, the second half the same up rows
+          const CUtensorMap* mu = &maps.m[q.b_up[seg]];
+          const int n = t.tn * kFeat;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          int n;
-          const CUtensorMap* mj = mb;
-          if (kEpi == kFfnGlu) {  // the first half of the tile's columns are gate rows, the second the same up rows
-            const bool up = kPair ? rank == 1 : j == 1;
-            n = t.tn * kFeat + (kPair ? 64 * j : 0);
-            if (up) mj = &maps.m[q.b[seg] - q.b[0] + q.b_up];
-          } else {
-            n = t.tn * TN + 128 * (int)rank + 64 * j;
+          for (int j = 0; j < 2; ++j) {
+            if (kPair) {
+              load_box<kPair>(sb + j * kBox, rank ? mu : mb, fb, k + 64 * j, n, q.b_plane[seg]);
+            } else {
+              load_box<kPair>(sb + j * kBox, mb, fb, k + 64 * j, n, q.b_plane[seg]);
+              load_box<kPair>(sb + j * kBox + kBox / 2, mu, fb, k + 64 * j, n, q.b_plane[seg]);
+            }
           }
-          load_box<kPair>(sa + (2 + j) * kBox, mj, fb, q.b_mn ? n : k, q.b_mn ? k : n, q.b_plane[seg]);
+        } else {
+          const int n = t.tn * TN + 128 * (int)rank;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            load_box<kPair>(sb + j * kBox, mb, fb, q.b_mn ? n + 64 * j : k + 64 * j, q.b_mn ? k : n, q.b_plane[seg]);
         }
         ++issued;
         if (++stage == kStages) { stage = 0; phase ^= 1u; }
@@ -206,8 +250,10 @@ ffn_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
       const Unit t = unit_of(a, u);
       const Prob& q = a.prob[t.p];
       const uint32_t idesc = tc::idesc_f16(TM, TN, a.ab_bf16 != 0, q.a_mn != 0, q.b_mn != 0);
-      // a K16 step: 32 bytes inside the swizzled row (K-major) or 16 rows of 128 bytes (MN-major)
+      // a K16 step: 32 bytes inside the swizzled row (K-major; its second 64 columns in the next box) or 16 rows of
+      // 128 bytes (MN-major)
       const uint32_t a_step = q.a_mn ? 2048 >> 4 : 32 >> 4, b_step = q.b_mn ? 2048 >> 4 : 32 >> 4;
+      const uint32_t a_far = q.a_mn ? 4 * 2048 >> 4 : kBox >> 4, b_far = q.b_mn ? 4 * 2048 >> 4 : kBox >> 4;
       if (!tc::mbar_wait(&acc_empty[buf], acc_phase ^ 1u, abort_flag)) { ok = false; break; }
       tc::fence_after_sync();
       const uint32_t dt = tmem + (uint32_t)(buf * TN);
@@ -220,8 +266,9 @@ ffn_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk) {
           const uint32_t acc = i > t.kb0 || kk > 0;
-          if (kPair) tc::mma_f16_pair(dt, da + kk * a_step, db + kk * b_step, idesc, acc);
-          else tc::mma_f16(dt, da + kk * a_step, db + kk * b_step, idesc, acc);
+          const uint64_t dak = da + (kk & 3) * a_step + (kk >> 2) * a_far, dbk = db + (kk & 3) * b_step + (kk >> 2) * b_far;
+          if (kPair) tc::mma_f16_pair(dt, dak, dbk, idesc, acc);
+          else tc::mma_f16(dt, dak, dbk, idesc, acc);
         }
         if (kPair) tc::mma_commit_pair(&empty[stage], 0x3);
         else tc::mma_commit(&empty[stage]);
@@ -243,67 +290,77 @@ ffn_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
     tc::mbar_wait(drain, 0, &never);
   } else if (warp >= 2) {
     // ---------------------------------------------------------------- epilogue (both CTAs)
-    const int q4 = warp & 3, half = (warp - 2) >> 2;
+    const int q4 = warp & 3, part = (warp - 2) >> 2;
     const uint32_t acc_empty0 = kPair ? tc::map_shared(tc::smem_u32(acc_empty), 0u) : 0u;
-    int buf = 0;
+    uint8_t* staged = smem + kStages * kStageBytes + (warp - 2) * kBlocks * kBlock;
+    int buf = 0, turn = 0;
     uint32_t acc_phase = 0;
     for (int u = first; u < a.units; u += step) {
       const Unit t = unit_of(a, u);
       const Prob& q = a.prob[t.p];
-      const int m = t.tm * TM + 128 * (int)rank + 32 * q4 + lane;
-      const int n0 = t.tn * kFeat + half * (kFeat / 2);
+      const int mw = t.tm * TM + 128 * (int)rank + 32 * q4, m = mw + lane;
+      const int n0 = t.tn * kFeat + part * kPart;
+      uint4 ng[4], nu[4];  // kFfnDglu: gate and up of the next block
+      auto fetch = [&](int c) {
+        const size_t at = (size_t)m * q.N + n0 + c;
+        load_row<T>((const T*)a.in1 + at, m < q.M, q.N - n0 - c, ng);
+        load_row<T>((const T*)a.in2 + at, m < q.M, q.N - n0 - c, nu);
+      };
+      if (kEpi == kFfnDglu) fetch(0);
       if (!tc::mbar_wait(&acc_full[buf], acc_phase, abort_flag)) {
         *abort_flag = 1;
         atomicOr(a.st, ST_TIMEOUT);
         break;
       }
       tc::fence_after_sync();
-      const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(buf * TN + half * (kFeat / 2));
+      const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(buf * TN + part * kPart);
 #pragma unroll 1
-      for (int c = 0; c < kFeat / 2; c += 32) {
+      for (int c = 0; c < kPart; c += 32) {
         uint32_t ra[32], rb[32];
         tc::tmem_ld_32x32b_x32(taddr + c, ra);
         if (kEpi == kFfnGlu) tc::tmem_ld_32x32b_x32(taddr + TN / 2 + c, rb);
         tc::tmem_ld_wait(ra);
         if (kEpi == kFfnGlu) tc::tmem_ld_wait(rb);
-        const int n = n0 + c, left = q.N - n;
-        if (m < q.M && left > 0) {
-          const size_t at = (size_t)m * q.N + n;
-          float v[32];
+        const int n = n0 + c;
+        float v[32], w[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(ra[i]);
-          if (kEpi == kFfnGlu) {
-            float w[32];
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(ra[i]);
+        const bool some = mw < q.M && n < q.N;  // the same in the whole warp
+        if (kEpi == kFfnGlu) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = __uint_as_float(rb[i]);
-            if (a.out2) store_row<T>((T*)a.out2 + at, v, left);
-            if (a.out3) store_row<T>((T*)a.out3 + at, w, left);
+          for (int i = 0; i < 32; ++i) w[i] = __uint_as_float(rb[i]);
+          if (some) {
+            if (a.out2 >= 0) store_block<T>(&maps.o[a.out2], staged, turn, lane, v, n, mw, 0);
+            if (a.out3 >= 0) store_block<T>(&maps.o[a.out3], staged, turn, lane, w, n, mw, 0);
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], a.act) * w[i];
-            store_row<T>((T*)q.out + at, v, left);
-          } else if (kEpi == kFfnDglu) {
-            constexpr int V = 16 / (int)sizeof(T);
-#pragma unroll
-            for (int i = 0; i < 32 / V; ++i)
-              if (i * V < left) {
-                float g[V], w[V], dg[V], du[V];
-                load_vec<T, V>((const T*)a.in1 + at + i * V, g);
-                load_vec<T, V>((const T*)a.in2 + at + i * V, w);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                  float slope;
-                  const float act = act_both(g[j], a.act, slope);
-                  dg[j] = v[i * V + j] * w[j] * slope;
-                  du[j] = v[i * V + j] * act;
-                }
-                store_vec<T, V>((T*)q.out + at + i * V, dg);
-                store_vec<T, V>((T*)a.out2 + at + i * V, du);
-              }
-          } else if (q.split > 1) {
-            store_row<float>(q.part + (size_t)t.s * q.M * q.N + at, v, left);
-          } else {
-            store_row<T>((T*)q.out + at, v, left);
+            store_block<T>(&maps.o[q.out], staged, turn, lane, v, n, mw, 0);
           }
+        } else if (kEpi == kFfnDglu) {
+          uint4 cg[4], cu[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) { cg[i] = ng[i]; cu[i] = nu[i]; }
+          if (c + 32 < kPart) fetch(c + 32);
+          if (some) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              T tg[8], tu[8];
+              memcpy(tg, &cg[i], 16);
+              memcpy(tu, &cu[i], 16);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                float slope;
+                const float act = act_both(to_f32(tg[j]), a.act, slope);
+                w[8 * i + j] = v[8 * i + j] * act;
+                v[8 * i + j] *= to_f32(tu[j]) * slope;
+              }
+            }
+            store_block<T>(&maps.o[q.out], staged, turn, lane, v, n, mw, 0);
+            store_block<T>(&maps.o[a.out2], staged, turn, lane, w, n, mw, 0);
+          }
+        } else if (some) {
+          if (q.split > 1) store_block<float>(&maps.o[q.out], staged, turn, lane, v, n, mw, t.s);
+          else store_block<T>(&maps.o[q.out], staged, turn, lane, v, n, mw, 0);
         }
       }
       tc::fence_before_sync();
@@ -315,6 +372,7 @@ ffn_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
       }
       if (++buf == 2) { buf = 0; acc_phase ^= 1u; }
     }
+    if (lane == 0) tc::bulk_wait_all();
   }
   tc::fence_before_sync();
   if (kPair) tc::cluster_sync();  // no CTA leaves while the other may still signal its barriers or read its operands
@@ -342,7 +400,7 @@ ffn_reduce_kernel(const __grid_constant__ Args a) {
         const float4 w = __ldcs(reinterpret_cast<const float4*>(q.part + s * n + i));
         v[0] += w.x; v[1] += w.y; v[2] += w.z; v[3] += w.w;
       }
-      store_vec<T, 4>((T*)q.out + i, v);
+      store_vec<T, 4>((T*)q.dst + i, v);
     }
   }
 }
@@ -368,15 +426,15 @@ Plan make_plan(const FfnLaunch& l, Args* a) {
     const FfnProblem& q = l.prob[p];
     const int kbs = ceil_div(q.K, BK), nkb = kbs * q.nseg;
     long long split = l.epi == kFfnStore && total < slots ? slots / total : 1;
-    if (split > nkb / 4) split = nkb / 4;
+    if (split > nkb / 2) split = nkb / 2;
     split = split < 1 ? 1 : split > kMaxSplit ? kMaxSplit : split;
     if (a) {
       Prob& r = a->prob[p];
       r.M = q.M; r.N = q.N; r.kbs = kbs; r.nkb = nkb; r.a_mn = q.a_mn; r.b_mn = q.b_mn;
-      for (int s = 0; s < 12; ++s) { r.a[s] = q.a[s]; r.b[s] = q.b[s]; r.a_plane[s] = q.a_plane[s]; r.b_plane[s] = q.b_plane[s]; }
-      r.b_up = q.b_up;
+      for (int s = 0; s < 12; ++s) { r.a[s] = q.a[s]; r.b[s] = q.b[s]; r.a_plane[s] = q.a_plane[s]; r.b_plane[s] = q.b_plane[s]; r.b_up[s] = q.b_up[s]; }
       r.tiles_m = ceil_div(q.M, t); r.tiles_n = ceil_div(q.N, t / feat); r.split = (int)split; r.begin = (int)units;
-      r.out = q.out;
+      r.out = p;
+      r.dst = q.out;
       r.part = (float*)off;  // an offset until the launch knows the workspace
     }
     units += tiles(q, t) * split;
@@ -390,8 +448,9 @@ Plan make_plan(const FfnLaunch& l, Args* a) {
   return pl;
 }
 
-bool encode_planes(CUtensorMap* map, const FfnOperand& o, int dtype) {
-  return encode_tmap_3d_planes(map, o.p, dtype, (uint64_t)o.cols, (uint64_t)o.rows, (uint64_t)o.planes, 64, 64);
+// Boxes of 128 rows; of 64 for the weights of a one-CTA gate and up tile, which has 64 rows of each.
+bool encode_planes(CUtensorMap* map, const FfnOperand& o, int dtype, bool small) {
+  return encode_tmap_3d_planes(map, o.p, dtype, (uint64_t)o.cols, (uint64_t)o.rows, (uint64_t)o.planes, 64, small ? 64 : 128);
 }
 
 int device_sms() {
@@ -403,11 +462,11 @@ int device_sms() {
 template <bool kPair, int kEpi, class T>
 cudaError_t go(const Maps& maps, const Args& a, cudaStream_t s) {
   auto kernel = ffn_tc_kernel<kPair, kEpi, T>;
-  cudaError_t e = set_max_dynamic_smem((const void*)kernel, kSmemBytes);
+  cudaError_t e = set_max_dynamic_smem((const void*)kernel, smem_bytes(kPair));
   if (e != cudaSuccess) return e;
   const int slots = kPair ? device_sms() / 2 : device_sms();
   const int n = a.units < slots ? a.units : slots;
-  e = launch_dependent(kernel, dim3((unsigned)(kPair ? 2 * n : n)), dim3(kThreads), kSmemBytes, s, kPair ? 2 : 1, maps, a);
+  e = launch_dependent(kernel, dim3((unsigned)(kPair ? 2 * n : n)), dim3(block_threads(kPair)), smem_bytes(kPair), s, kPair ? 2 : 1, maps, a);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }
@@ -438,14 +497,29 @@ size_t ffn_tc_partial_bytes(const FfnLaunch& l) { return make_plan(l, nullptr).p
 
 cudaError_t launch_ffn_tc(const FfnLaunch& l, float* partial, unsigned* st, cudaStream_t s) {
   Maps maps;
-  for (int i = 0; i < l.nop; ++i)
-    if (!encode_planes(&maps.m[i], l.op[i], l.op_dtype)) return cudaErrorInvalidValue;
   Args a{};
   const Plan pl = make_plan(l, &a);
+  for (int i = 0; i < l.nop; ++i)
+    if (!encode_planes(&maps.m[i], l.op[i], l.op_dtype, l.epi == kFfnGlu && !pl.pair && i > 0)) return cudaErrorInvalidValue;
   for (int p = 0; p < a.nprob; ++p) a.prob[p].part = (float*)((char*)partial + (size_t)a.prob[p].part);
   a.act = l.act;
   a.ab_bf16 = l.op_dtype == SWIMBA_BF16;
-  a.out2 = l.out2; a.out3 = l.out3; a.in1 = l.in1; a.in2 = l.in2;
+  // outputs: one map per problem (of its partial sums where it is split), then the other two
+  for (int p = 0; p < a.nprob; ++p) {
+    const Prob& q = a.prob[p];
+    const bool ok = q.split > 1 ? encode_tmap_3d_planes(&maps.o[p], q.part, SWIMBA_F32, q.N, q.M, q.split, 16, 32)
+                                : encode_tmap_3d_planes(&maps.o[p], q.dst, l.dtype, q.N, q.M, 1, 32, 32);
+    if (!ok) return cudaErrorInvalidValue;
+  }
+  void* more[2] = {l.out2, l.out3};
+  int at[2] = {-1, -1};
+  for (int i = 0; i < 2; ++i)
+    if (more[i]) {
+      at[i] = kFfnMaxProblems + i;
+      if (!encode_tmap_3d_planes(&maps.o[at[i]], more[i], l.dtype, a.prob[0].N, a.prob[0].M, 1, 32, 32))
+        return cudaErrorInvalidValue;
+    }
+  a.out2 = at[0]; a.out3 = at[1]; a.in1 = l.in1; a.in2 = l.in2;
   a.st = st;
   return l.dtype == SWIMBA_BF16 ? go_type<__nv_bfloat16>(l, pl, maps, a, s) : go_type<__half>(l, pl, maps, a, s);
 }

@@ -25,8 +25,8 @@ struct FfnProblem {
   int M, N, K;       // K of one segment
   int a_mn, b_mn;    // the operand's rows are K (its columns M or N), not M or N
   int nseg;
-  unsigned char a[12], a_plane[12], b[12], b_plane[12];  // kFfnGlu: b is the gate's weights, b_up the up weights
-  unsigned char b_up;
+  unsigned char a[12], a_plane[12], b[12], b_plane[12];
+  unsigned char b_up[12];  // kFfnGlu: the up weights, where b is the gate's (operand 0 is x)
   void* out;         // [M][N] (kFfnGlu: h, kFfnDglu: dgate)
 };
 

@@ -224,7 +224,7 @@ FfnLaunch glu_launch(const FfnDims& d, const void* x, const void* wg, const void
   l.op[0] = {x, d.M, d.D, 1}; l.op[1] = {wg, d.F, d.D, 1}; l.op[2] = {wu, d.F, d.D, 1};
   l.nprob = 1;
   l.prob[0] = problem(d.M, d.F, d.D, 0, false, 1, false, h);
-  l.prob[0].b_up = 2;
+  l.prob[0].b_up[0] = 2;
   l.out2 = gate; l.out3 = up;
   return l;
 }

@@ -69,6 +69,18 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 // Orders this thread's earlier generic-proxy global accesses (an acquire of a flag) before its later
 // async-proxy global accesses (a bulk copy of the data the flag guards).
 __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+// 3D tiled bulk copy from this CTA's shared memory, in the thread's current bulk group; out-of-range elements of the
+// box are not written.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"((uint64_t)map),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// Waits until at most N of this thread's bulk groups have still to read their shared memory (or, all: to finish).
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)map) : "memory");
 }
@@ -278,7 +290,8 @@ bool encode_tmap_2d(CUtensorMap* map, const void* base, int dtype, uint64_t cols
 // selects one slot of box_rows consecutive rows.
 bool encode_tmap_3d_slot(CUtensorMap* map, const void* base, int dtype, uint64_t cols, uint64_t slots, uint64_t rows,
                          uint32_t box_cols, uint32_t box_rows);
-// Host: 3D map of [planes][rows][cols] (dims {cols, rows, planes}); box {box_cols, box_rows, 1} in one plane.
+// Host: 3D map of [planes][rows][cols] (dims {cols, rows, planes}); box {box_cols, box_rows, 1} in one plane, its rows
+// of 128 or 64 bytes swizzled over as many bytes.
 bool encode_tmap_3d_planes(CUtensorMap* map, const void* base, int dtype, uint64_t cols, uint64_t rows, uint64_t planes,
                            uint32_t box_cols, uint32_t box_rows);
 

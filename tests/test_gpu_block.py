@@ -361,7 +361,9 @@ def test_gated_scan_extreme_gates():
 
 # ------------------------------------------------------------------------------------------------ feed-forward
 FFN_SHAPES = [(1, 64, 128), (1, 8, 8), (3, 72, 40), (16, 256, 512), (17, 128, 264), (100, 320, 200), (128, 64, 64), (129, 200, 136),
-              (300, 768, 2048), (257, 520, 1032)]
+              (300, 768, 2048), (257, 520, 1032),
+              # tiles enough for CTA pairs in every product of one of the two, ragged in all three sizes
+              (1500, 264, 2056), (5000, 520, 264)]
 # longest chain of fp32 adds of a product over K: each of the K terms may be added one after the other, and the
 # tensor cores may cut an addend's last bits instead of rounding them, 2 u a term
 def dot_bound(a, b):
