@@ -6,8 +6,9 @@
 
 namespace swimba {
 
-__device__ __forceinline__ float act_both(float g, int act, float& slope) {
-  if (act == SWIMBA_SILU) {
+template <int kAct>
+__device__ __forceinline__ float act_both(float g, float& slope) {
+  if (kAct == SWIMBA_SILU) {
     float s, q;
     gate_pair(g, s, q);
     slope = s * fmaf(g, q, 1.f);
@@ -18,9 +19,10 @@ __device__ __forceinline__ float act_both(float g, int act, float& slope) {
   return g * c;
 }
 
-// .
-__device__ __forceinline__ float act_value(float g, int act) {
-  if (act == SWIMBA_SILU) return g * rcp_fast(1.f + exp_fast(-g));
+// The value alone: silu's quotient is 0 where exp(-g) overflows.
+template <int kAct>
+__device__ __forceinline__ float act_value(float g) {
+  if (kAct == SWIMBA_SILU) return g * rcp_fast(1.f + exp_fast(-g));
   return g * (0.5f * (1.f + erff(g * 0.70710678f)));
 }
 

@@ -50,9 +50,9 @@ __device__ __forceinline__ void fetch(const T* p, long long ld, int rows, int K,
   if (r < rows && k < K) load_vec<T, 4>(KC ? p + (size_t)r * ld + k : p + (size_t)k * ld + r, v);
 }
 
-template <class T, bool AKC, bool BKC, int EPI>
+template <class T, bool AKC, bool BKC, int EPI, int kAct>
 __global__ void __launch_bounds__(kThreads)
-ffn_simt_kernel(int M, int N, int K, int nsum, int act, Operand<T> A, Operand<T> B, Out<T> o) {
+ffn_simt_kernel(int M, int N, int K, int nsum, Operand<T> A, Operand<T> B, Out<T> o) {
   __shared__ float As[2][BK][BT + 4], Bs[2][BK][BT + 4];
   const int tid = threadIdx.x;
   constexpr int kCols = EPI == kGlu ? BT / 2 : BT;  // features per tile
@@ -128,7 +128,7 @@ ffn_simt_kernel(int M, int N, int K, int nsum, int act, Operand<T> A, Operand<T>
       if (n >= N) break;
       float g[4], u[4], h[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) { g[j] = acc[i][j]; u[j] = acc[i][j + 4]; h[j] = act_value(g[j], act) * u[j]; }
+      for (int j = 0; j < 4; ++j) { g[j] = acc[i][j]; u[j] = acc[i][j + 4]; h[j] = act_value<kAct>(g[j]) * u[j]; }
       store_vec<T, 4>(o.a + (size_t)m * o.ld + n, h);
       if (o.b) store_vec<T, 4>(o.b + (size_t)m * o.ld + n, g);
       if (o.c) store_vec<T, 4>(o.c + (size_t)m * o.ld + n, u);
@@ -147,7 +147,7 @@ ffn_simt_kernel(int M, int N, int K, int nsum, int act, Operand<T> A, Operand<T>
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             float slope;
-            const float a = act_both(g[j], act, slope);
+            const float a = act_both<kAct>(g[j], slope);
             dg[j] = v[j] * u[j] * slope;
             du[j] = v[j] * a;
           }
@@ -164,7 +164,10 @@ ffn_simt_kernel(int M, int N, int K, int nsum, int act, Operand<T> A, Operand<T>
 template <class T, bool AKC, bool BKC, int EPI>
 cudaError_t product(int M, int N, int K, int nsum, int act, Operand<T> A, Operand<T> B, Out<T> o, cudaStream_t s) {
   const dim3 grid(ceil_div(M, BT), ceil_div(N, EPI == kGlu ? BT / 2 : BT));
-  ffn_simt_kernel<T, AKC, BKC, EPI><<<grid, kThreads, 0, s>>>(M, N, K, nsum, act, A, B, o);
+  if (EPI == kStore || act == SWIMBA_SILU)
+    ffn_simt_kernel<T, AKC, BKC, EPI, SWIMBA_SILU><<<grid, kThreads, 0, s>>>(M, N, K, nsum, A, B, o);
+  else
+    ffn_simt_kernel<T, AKC, BKC, EPI, SWIMBA_GELU><<<grid, kThreads, 0, s>>>(M, N, K, nsum, A, B, o);
   count_launches(1);
   return cudaGetLastError();
 }
