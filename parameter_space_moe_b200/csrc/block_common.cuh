@@ -135,10 +135,10 @@ cudaError_t launch_layer_norm_bwd(const NormDims& d, const void* r, const float*
                                   void* dx, float* dgamma, float* dbeta, float* part, cudaStream_t s);
 
 cudaError_t launch_gated_scan(const GatedDims& d, const void* x, const void* gate, const float* init, void* h,
-                              float* final_state, cudaStream_t s);
+                              float* final_state, unsigned* st, cudaStream_t s);
 cudaError_t launch_gated_scan_bwd(const GatedDims& d, const void* x, const void* gate, const void* h, const float* init,
                                   const void* dh, const float* dfinal, void* dx, void* dgate, float* dinit,
-                                  cudaStream_t s);
+                                  unsigned* st, cudaStream_t s);
 cudaError_t launch_gated_step(const GatedDims& d, const void* x, const void* gate, float* state, void* h,
                               cudaStream_t s);
 

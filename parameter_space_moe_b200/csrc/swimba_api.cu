@@ -627,9 +627,11 @@ swimba_status swimba_gated_scan(const swimba_gated_dims* dims, const void* x, co
   SW_TRY(make_gated_dims(dims, &d));
   if (!ok_ptr(x) || !ok_ptr(gate) || !ok_opt(init_state) || !ok_ptr(h) || !ok_opt(final_state))
     return SWIMBA_ERR_INVALID_ARG;
+  unsigned* st = device_status();
+  if (!st) return SWIMBA_ERR_CUDA;
   cudaStream_t s = (cudaStream_t)stream;
   prof_begin(s);
-  SW_CUDA(launch_gated_scan(d, x, gate, init_state, h, final_state, s));
+  SW_CUDA(launch_gated_scan(d, x, gate, init_state, h, final_state, st, s));
   prof_mark(s, "gated_scan");
   return SWIMBA_OK;
 }
@@ -642,9 +644,11 @@ swimba_status swimba_gated_scan_bwd(const swimba_gated_dims* dims, const void* x
   if (!ok_ptr(x) || !ok_ptr(gate) || !ok_ptr(h) || !ok_opt(init_state) || !ok_ptr(dh) || !ok_opt(d_final) ||
       !ok_ptr(dx) || !ok_ptr(dgate) || !ok_opt(d_init))
     return SWIMBA_ERR_INVALID_ARG;
+  unsigned* st = device_status();
+  if (!st) return SWIMBA_ERR_CUDA;
   cudaStream_t s = (cudaStream_t)stream;
   prof_begin(s);
-  SW_CUDA(launch_gated_scan_bwd(d, x, gate, h, init_state, dh, d_final, dx, dgate, d_init, s));
+  SW_CUDA(launch_gated_scan_bwd(d, x, gate, h, init_state, dh, d_final, dx, dgate, d_init, st, s));
   prof_mark(s, "gated_scan_bwd");
   return SWIMBA_OK;
 }
