@@ -8,7 +8,7 @@
 // A step is the linear map c -> a c + b of the carried value c (forward: a = f, b = (1 - f) x, c = h; backward,
 // from the last token: a = f, b = f dh, c = f_{t+1} lambda_{t+1}), and maps compose: (a2, b2) after (a1, b1) is
 // (a2 a1, a2 b1 + b2).  A cluster of CTAs owns 32 V columns of one sequence.  Per round it covers
-// (CTAs x kWarps x S) consecutive tokens: each warp composes the maps of its S tokens in registers, the warps'
+// (CTAs x warps x S) consecutive tokens: each warp composes the maps of its S tokens in registers, the warps'
 // maps meet in shared memory, the CTAs' in distributed shared memory (asynchronous stores counted on an mbarrier: a
 // cluster barrier would first wait for the round's stores of h), and every warp then replays its tokens from its true
 // carried value.  So each input is read once, the split along time needs no pass over memory, no workspace and no
@@ -22,88 +22,71 @@ namespace swimba {
 
 namespace {
 
-#ifndef KW
-#define KW 4
-#define KST 3
-#endif
-constexpr int kWarps = KW, kStages = KST;
-constexpr int kMaxCluster = 8;
+constexpr int kWarps = 4, kStages = 2;
 
-// Two-wide fp32 arithmetic for pairs of columns.
-__device__ __forceinline__ unsigned long long f2(float a, float b) {
-  unsigned long long r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void un2(unsigned long long v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
+// fp32 arithmetic on a lane's V columns; a pair of columns lives in one 64-bit register pair, where the two-wide
+// instructions take it.
 template <int V>
-struct Vec {
-  float v[V];
+struct Vec;
+template <>
+struct Vec<1> {
+  float p;
+  __device__ __forceinline__ Vec() {}
+  __device__ __forceinline__ explicit Vec(const float (&v)[1]) : p(v[0]) {}
+  __device__ __forceinline__ void out(float (&v)[1]) const { v[0] = p; }
 };
-template <int V>
-__device__ __forceinline__ Vec<V> operator*(const Vec<V>& a, const Vec<V>& b) {
-  Vec<V> r;
-  if constexpr (V == 2) {
-    unsigned long long d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f2(a.v[0], a.v[1])), "l"(f2(b.v[0], b.v[1])));
-    un2(d, r.v[0], r.v[1]);
-  } else {
-    r.v[0] = a.v[0] * b.v[0];
-  }
-  return r;
+template <>
+struct Vec<2> {
+  unsigned long long p;
+  __device__ __forceinline__ Vec() {}
+  __device__ __forceinline__ explicit Vec(const float (&v)[2]) { asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(v[0]), "f"(v[1])); }
+  __device__ __forceinline__ void out(float (&v)[2]) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(v[0]), "=f"(v[1]) : "l"(p)); }
+};
+__device__ __forceinline__ Vec<1> operator*(Vec<1> a, Vec<1> b) { a.p *= b.p; return a; }
+__device__ __forceinline__ Vec<1> operator+(Vec<1> a, Vec<1> b) { a.p += b.p; return a; }
+__device__ __forceinline__ Vec<1> fma(Vec<1> a, Vec<1> b, Vec<1> c) { a.p = fmaf(a.p, b.p, c.p); return a; }
+__device__ __forceinline__ Vec<2> operator*(Vec<2> a, Vec<2> b) {
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a.p) : "l"(b.p));
+  return a;
 }
-template <int V>
-__device__ __forceinline__ Vec<V> operator+(const Vec<V>& a, const Vec<V>& b) {
-  Vec<V> r;
-  if constexpr (V == 2) {
-    unsigned long long d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f2(a.v[0], a.v[1])), "l"(f2(b.v[0], b.v[1])));
-    un2(d, r.v[0], r.v[1]);
-  } else {
-    r.v[0] = a.v[0] + b.v[0];
-  }
-  return r;
+__device__ __forceinline__ Vec<2> operator+(Vec<2> a, Vec<2> b) {
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a.p) : "l"(b.p));
+  return a;
 }
-template <int V>
-__device__ __forceinline__ Vec<V> fma(const Vec<V>& a, const Vec<V>& b, const Vec<V>& c) {
-  Vec<V> r;
-  if constexpr (V == 2) {
-    unsigned long long d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(d)
-        : "l"(f2(a.v[0], a.v[1])), "l"(f2(b.v[0], b.v[1])), "l"(f2(c.v[0], c.v[1])));
-    un2(d, r.v[0], r.v[1]);
-  } else {
-    r.v[0] = fmaf(a.v[0], b.v[0], c.v[0]);
-  }
-  return r;
+__device__ __forceinline__ Vec<2> fma(Vec<2> a, Vec<2> b, Vec<2> c) {
+  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(a.p) : "l"(b.p), "l"(c.p));
+  return a;
 }
 template <int V>
 __device__ __forceinline__ Vec<V> all(float x) {
-  Vec<V> r;
+  float v[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) r.v[i] = x;
-  return r;
+  for (int i = 0; i < V; ++i) v[i] = x;
+  return Vec<V>(v);
 }
 
 // gate_pair for V columns.
 template <int V>
-__device__ __forceinline__ void gates(const Vec<V>& g, Vec<V>& f, Vec<V>& q) {
-  Vec<V> e, r;
+__device__ __forceinline__ void gates(const float (&g)[V], Vec<V>& f, Vec<V>& q) {
+  float e[V], r[V], s[V], l[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) e.v[i] = exp_fast(-fabsf(g.v[i]));
-  const Vec<V> d = e + all<V>(1.f);
+  for (int i = 0; i < V; ++i) e[i] = exp_fast(-fabsf(g[i]));
+  const Vec<V> ev(e);
+  (ev + all<V>(1.f)).out(r);
 #pragma unroll
-  for (int i = 0; i < V; ++i) r.v[i] = rcp_fast(d.v[i]);
-  const Vec<V> small = e * r, large = fma(small, all<V>(-1.f), all<V>(1.f));
+  for (int i = 0; i < V; ++i) r[i] = rcp_fast(r[i]);
+  const Vec<V> small = ev * Vec<V>(r), large = fma(small, all<V>(-1.f), all<V>(1.f));
+  small.out(s);
+  large.out(l);
+  float fo[V], qo[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const bool open = g.v[i] >= 0.f;
-    f.v[i] = open ? large.v[i] : small.v[i];
-    q.v[i] = open ? small.v[i] : large.v[i];
+    const bool open = g[i] >= 0.f;
+    fo[i] = open ? l[i] : s[i];
+    qo[i] = open ? s[i] : l[i];
   }
+  f = Vec<V>(fo);
+  q = Vec<V>(qo);
 }
 
 // The map of some consecutive steps, for a lane's V columns.
@@ -117,9 +100,10 @@ __device__ __forceinline__ void then(Map<V>& m, const Vec<V>& a, const Vec<V>& b
   m.a = a * m.a;
 }
 
-// A round's maps: this CTA's warps and, by CTA rank, the cluster's CTAs.  Two copies, used in turn: a warp writes a copy
-// again two rounds later, after a block barrier (or, from another CTA, after this CTA's map of the round between) that
-// follows every read of it.
+// A round's maps: this CTA's warps and, by CTA rank, the cluster's CTAs.  Two copies, used in turn: a warp writes one
+// again two rounds later, after a block barrier (another CTA: after this CTA's map of the round between, sent behind one)
+// that follows every read of it.
+constexpr int kMaxCluster = 16;
 template <int V>
 struct alignas(16) Maps {
   Map<V> warp[2][kWarps][32];
@@ -145,24 +129,22 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
 
 // Every thread, before the first round.
 template <int V>
-__device__ __forceinline__ void exchange_init(Maps<V>& sm, uint32_t nrank) {
-  if (nrank == 1) return;
+__device__ __forceinline__ void exchange_init(Maps<V>& sm) {
   if (threadIdx.x == 0) {
-    tc::mbar_init(&sm.bar[0], 1);
-    tc::mbar_init(&sm.bar[1], 1);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(&sm.bar[i], 1);
     tc::fence_barrier_init();
   }
   tc::cluster_sync();  // every CTA runs, its barriers initialised, before another stores to its shared memory
 }
 
-// Given this warp's map of round `round`, returns the carried value in front of the warp's first token and advances
-// `carry` over the whole round.
+// Sends round `round`'s maps on their way, given the map `mine` of this warp's tokens.  Returns the map of the CTA's tokens
+// in front of them.
 template <int V>
-__device__ __forceinline__ Vec<V> exchange(Maps<V>& sm, int round, int warp, int lane, uint32_t rank, uint32_t nrank,
-                                           const Map<V>& mine, Vec<V>& carry, unsigned* st) {
+__device__ __forceinline__ Map<V> send(Maps<V>& sm, int round, int warp, int lane, uint32_t rank, uint32_t nrank,
+                                       const Map<V>& mine) {
   const int buf = round & 1;
   sm.warp[buf][warp][lane] = mine;
-  if (nrank > 1 && threadIdx.x == 0) tc::mbar_arrive_expect_tx(&sm.bar[buf], nrank * 32 * (uint32_t)sizeof(Map<V>));
+  if (threadIdx.x == 0) tc::mbar_arrive_expect_tx(&sm.bar[buf], nrank * 32 * (uint32_t)sizeof(Map<V>));
   __syncthreads();
   Map<V> before;
   before.a = all<V>(1.f);
@@ -173,42 +155,43 @@ __device__ __forceinline__ Vec<V> exchange(Maps<V>& sm, int round, int warp, int
       const Map<V> m = sm.warp[buf][w][lane];
       then(before, m.a, m.b);
     }
-  if (nrank == 1) {
-    const Vec<V> start = fma(before.a, carry, before.b);
-    carry = fma(mine.a, start, mine.b);
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w)
-      if (w > warp) {
-        const Map<V> m = sm.warp[buf][w][lane];
-        carry = fma(m.a, carry, m.b);
-      }
-    return start;
-  }
   if (warp == kWarps - 1) {
-    Map<V> whole = before;
-    then(whole, mine.a, mine.b);
+    Map<V> cta = before;
+    then(cta, mine.a, mine.b);
     const uint32_t at = tc::smem_u32(&sm.cta[buf][rank][lane]), bar = tc::smem_u32(&sm.bar[buf]);
+    float a[V], b[V];
+    cta.a.out(a);
+    cta.b.out(b);
     for (uint32_t r = 0; r < nrank; ++r) {
       const uint32_t to = tc::map_shared(at, r), on = tc::map_shared(bar, r);
       if constexpr (V == 2)
         asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
-                     "f"(whole.a.v[0]), "f"(whole.a.v[1]), "f"(whole.b.v[0]), "f"(whole.b.v[1]), "r"(on)
+                     "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]), "r"(on)
                      : "memory");
       else
         asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to),
-                     "f"(whole.a.v[0]), "f"(whole.b.v[0]), "r"(on)
+                     "f"(a[0]), "f"(b[0]), "r"(on)
                      : "memory");
     }
   }
+  return before;
+}
+
+// Takes round `round`'s maps: returns the carried value in front of this warp's tokens and advances `carry` over the
+// round.
+template <int V>
+__device__ __forceinline__ Vec<V> receive(Maps<V>& sm, int round, int lane, uint32_t rank, uint32_t nrank,
+                                          const Map<V>& before, Vec<V>& carry, unsigned* st) {
+  const int buf = round & 1;
   if (!wait_cluster(&sm.bar[buf], (uint32_t)(round >> 1) & 1u)) atomicOr(st, ST_TIMEOUT);
-  Vec<V> c = carry, start = carry;
-  for (uint32_t r = 0; r < nrank; ++r) {
-    if (r == rank) start = fma(before.a, c, before.b);
-    const Map<V> m = sm.cta[buf][r][lane];
-    c = fma(m.a, c, m.b);
+  Vec<V> c = carry, at = carry;
+  const Map<V>* m = sm.cta[buf][0] + lane;
+  for (uint32_t r = 0; r < nrank; ++r, m += 32) {
+    if (r == rank) at = c;
+    c = fma(m->a, c, m->b);
   }
   carry = c;
-  return start;
+  return fma(before.a, at, before.b);
 }
 
 // 16 bytes global -> shared.
@@ -219,7 +202,7 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// One warp's tokens of one input, from a stage in shared memory or from registers: 32 V columns of S rows.
+// One warp's tokens of one input, from a stage in shared memory or from registers: S rows of 32 V columns.
 template <class T, int V, int S, bool kAsync>
 struct Rows {
   static constexpr int kRowBytes = 32 * V * (int)sizeof(T);
@@ -243,7 +226,8 @@ struct Rows {
       } else {
 #pragma unroll
         for (int k = 0; k < S / kStep; ++k)
-          if (t + dir * k * kStep >= 0 && t + dir * k * kStep < n) cp_async16(to + k * kStep * kRowBytes, from + k * step);
+          if (t + dir * k * kStep >= 0 && t + dir * k * kStep < n)
+            cp_async16(to + k * kStep * kRowBytes, from + k * step);
       }
     } else {
       const int col = col0 + V * lane;
@@ -255,26 +239,27 @@ struct Rows {
       }
     }
   }
-  __device__ __forceinline__ Vec<V> get(const uint8_t* stage, int i, int lane) const {
-    Vec<V> out;
+  __device__ __forceinline__ void get(const uint8_t* stage, int i, int lane, float (&out)[V]) const {
     if constexpr (kAsync) {
-      load_vec<T, V>(reinterpret_cast<const T*>(stage + i * kRowBytes) + V * lane, out.v);
+      load_vec<T, V>(reinterpret_cast<const T*>(stage + i * kRowBytes) + V * lane, out);
     } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) out.v[v] = to_f32(raw[i][v]);
+      for (int v = 0; v < V; ++v) out[v] = to_f32(raw[i][v]);
     }
-    return out;
+  }
+  __device__ __forceinline__ Vec<V> get(const uint8_t* stage, int i, int lane) const {
+    float v[V];
+    get(stage, i, lane, v);
+    return Vec<V>(v);
   }
 };
 
 template <int V>
 __device__ __forceinline__ Vec<V> load_state(const float* p, size_t at, bool live) {
-  Vec<V> r = all<V>(0.f);
-  if (p && live) {
+  float r[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) r.v[v] = p[at + v];
-  }
-  return r;
+  for (int v = 0; v < V; ++v) r[v] = p && live ? p[at + v] : 0.f;
+  return Vec<V>(r);
 }
 
 template <class T, int V, int S, bool kAsync>
@@ -299,7 +284,7 @@ gated_scan_kernel(int T_, int W, int ngrp, long long xs, long long gs, const T* 
   h += row0 * W + col;
   const int span = (int)nrank * kWarps * S;
   R rx, rg;
-  int t = ((int)rank * kWarps + warp) * S;
+  int t = ((int)rank * kWarps + warp) * S;  // the warp's first token
   auto fetch = [&](int t, int st) {
     rx.fetch(stages + st * kStride, x, xs, t, 1, T_, col0, W, lane);
     rg.fetch(stages + st * kStride + R::kBytes, gate, gs, t, 1, T_, col0, W, lane);
@@ -308,7 +293,7 @@ gated_scan_kernel(int T_, int W, int ngrp, long long xs, long long gs, const T* 
 #pragma unroll
   for (int k = 0; k < (kAsync ? kStages - 1 : 1); ++k) fetch(t + k * span, k);
   Vec<V> carry = load_state<V>(init, state, live);
-  exchange_init(sm, nrank);
+  exchange_init(sm);
   int st = 0;
   for (int round = 0; round * span < T_; ++round, t += span) {
     if (kAsync) {
@@ -317,38 +302,55 @@ gated_scan_kernel(int T_, int W, int ngrp, long long xs, long long gs, const T* 
       cp_async_wait<kStages - 1>();
       __syncwarp();
     }
-    Vec<V> f[S], q[S];
-    Map<V> mine;
+    // a token's state is P c + H for the value c carried to the warp's tokens
+    Vec<V> P[S], H[S];
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-      gates(rg.get(stages + st * kStride + R::kBytes, i, lane), f[i], q[i]);
-      q[i] = q[i] * rx.get(stages + st * kStride, i, lane);
+      float g[V];
+      rg.get(stages + st * kStride + R::kBytes, i, lane, g);
+      gates(g, P[i], H[i]);
+      H[i] = H[i] * rx.get(stages + st * kStride, i, lane);
     }
     if (t + S > T_) {
 #pragma unroll
       for (int i = 0; i < S; ++i)
-        if (t + i >= T_) { f[i] = all<V>(1.f); q[i] = all<V>(0.f); }
+        if (t + i >= T_) { P[i] = all<V>(1.f); H[i] = all<V>(0.f); }
     }
-    mine.a = f[0];
-    mine.b = q[0];
 #pragma unroll
-    for (int i = 1; i < S; ++i) then(mine, f[i], q[i]);
+    for (int i = 1; i < S; ++i) {
+      H[i] = fma(P[i], H[i - 1], H[i]);
+      P[i] = P[i] * P[i - 1];
+    }
     if (!kAsync) fetch(t + span, 0);
-    Vec<V> c = exchange(sm, round, warp, lane, rank, nrank, mine, carry, status);
+    Map<V> mine;
+    mine.a = P[S - 1];
+    mine.b = H[S - 1];
+    const Map<V> before = send(sm, round, warp, lane, rank, nrank, mine);
+    const Vec<V> c = receive(sm, round, lane, rank, nrank, before, carry, status);
     T* out = h + (size_t)t * W;
+    auto put = [&](int n) {
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
-      c = fma(f[i], c, q[i]);
-      if (live && t + i < T_) store_vec<T, V>(out + (size_t)i * W, c.v);
+      for (int i = 0; i < S; ++i) {
+        float o[V];
+        fma(P[i], c, H[i]).out(o);
+        if (i < n) store_vec<T, V>(out, o);
+        out += W;
+      }
+    };
+    if (live) {
+      if (t + S <= T_) put(S);
+      else put(T_ - t);
     }
     st = st == kStages - 1 ? 0 : st + 1;
   }
   cp_async_wait<0>();
   if (final_state && live && rank == 0 && warp == 0) {
+    float o[V];
+    carry.out(o);
 #pragma unroll
-    for (int v = 0; v < V; ++v) final_state[state + v] = carry.v[v];
+    for (int v = 0; v < V; ++v) final_state[state + v] = o[v];
   }
-  if (nrank > 1) tc::cluster_sync();  // no CTA leaves while another may still store to it
+  tc::cluster_sync();  // no CTA leaves while another may still store to it
 }
 
 // Token index tau counts from the last token: t = T - 1 - tau.
@@ -380,7 +382,7 @@ gated_scan_bwd_kernel(int T_, int W, int ngrp, long long xs, long long gs, const
   const int span = (int)nrank * kWarps * S;
   R rx, rg, rh;
   RG rd;
-  int t = T_ - 1 - ((int)rank * kWarps + warp) * S;  // the warp's first (last) token
+  int t = T_ - 1 - ((int)rank * kWarps + warp) * S;  // the warp's last token
   auto fetch = [&](int t, int st) {
     uint8_t* p = stages + st * kStride;
     rg.fetch(p, gate, gs, t, -1, T_, col0, W, lane);
@@ -392,7 +394,7 @@ gated_scan_bwd_kernel(int T_, int W, int ngrp, long long xs, long long gs, const
 #pragma unroll
   for (int k = 0; k < (kAsync ? kStages - 1 : 1); ++k) fetch(t - k * span, k);
   Vec<V> carry = load_state<V>(dfinal, state, live);
-  exchange_init(sm, nrank);
+  exchange_init(sm);
   int st = 0;
   for (int round = 0; round * span < T_; ++round, t -= span) {
     if (kAsync) {
@@ -405,7 +407,9 @@ gated_scan_bwd_kernel(int T_, int W, int ngrp, long long xs, long long gs, const
     Map<V> mine;
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-      gates(rg.get(p, i, lane), f[i], q[i]);
+      float g[V];
+      rg.get(p, i, lane, g);
+      gates(g, f[i], q[i]);
       d[i] = rd.get(p + 3 * R::kBytes, i, lane);
       e[i] = fma(rx.get(p + R::kBytes, i, lane), all<V>(-1.f), rh.get(p + 2 * R::kBytes, i, lane));
     }
@@ -421,25 +425,30 @@ gated_scan_bwd_kernel(int T_, int W, int ngrp, long long xs, long long gs, const
 #pragma unroll
     for (int i = 1; i < S; ++i) then(mine, f[i], f[i] * d[i]);
     if (!kAsync) fetch(t - span, 0);
-    Vec<V> c = exchange(sm, round, warp, lane, rank, nrank, mine, carry, status);
+    const Map<V> before = send(sm, round, warp, lane, rank, nrank, mine);
+    Vec<V> c = receive(sm, round, lane, rank, nrank, before, carry, status);
 #pragma unroll
     for (int i = 0; i < S; ++i) {
       const Vec<V> lam = d[i] + c;
       c = f[i] * lam;
-      const Vec<V> ox = q[i] * lam, og = c * q[i] * e[i];
+      float ox[V], og[V];
+      (q[i] * lam).out(ox);
+      (c * q[i] * e[i]).out(og);
       if (live && t - i >= 0) {
-        store_vec<G, V>(dx + (size_t)(t - i) * W, ox.v);
-        store_vec<G, V>(dgate + (size_t)(t - i) * W, og.v);
+        store_vec<G, V>(dx + (size_t)(t - i) * W, ox);
+        store_vec<G, V>(dgate + (size_t)(t - i) * W, og);
       }
     }
     st = st == kStages - 1 ? 0 : st + 1;
   }
   cp_async_wait<0>();
   if (dinit && live && rank == 0 && warp == 0) {
+    float o[V];
+    carry.out(o);
 #pragma unroll
-    for (int v = 0; v < V; ++v) dinit[state + v] = carry.v[v];
+    for (int v = 0; v < V; ++v) dinit[state + v] = o[v];
   }
-  if (nrank > 1) tc::cluster_sync();
+  tc::cluster_sync();
 }
 
 // One token of every sequence: state <- f state + (1 - f) x, h = state.
@@ -466,111 +475,125 @@ gated_step_kernel(int B, int W, long long xs, long long gs, const T* __restrict_
   }
 }
 
-// CTAs per cluster: of the sizes that leave no CTA without a round, the one with the fewest rounds in a row, counting
-// the clusters that can be resident at once (asked once per kernel: GPCs of uneven size hold fewer CTAs in larger
-// clusters, and one cluster too many takes as long as a second set).
-struct Resident {
-  std::atomic<int> clusters[kMaxCluster + 1];
-};
-template <class K>
-int cluster_size(K kernel, Resident& seen, const GatedDims& d, int groups, int round_tokens, size_t smem) {
-  const int rounds = ceil_div(d.T, round_tokens);
-  int best = 1;
-  long long best_cost = 0;
-  for (int c = 1; c <= kMaxCluster && c <= rounds; ++c) {
-    int n = seen.clusters[c].load(std::memory_order_relaxed);
-    if (n == 0) {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3((unsigned)c * 1024);
-      cfg.blockDim = dim3(32 * kWarps);
-      cfg.dynamicSmemBytes = smem;
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = (unsigned)c;
-      attr[0].val.clusterDim.y = 1;
-      attr[0].val.clusterDim.z = 1;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
-        (void)cudaGetLastError();
-        n = 1;
-      }
-      seen.clusters[c].store(n, std::memory_order_relaxed);
-    }
-    const long long cost = (long long)ceil_div(groups, n) * ceil_div(rounds, c);
-    if (c == 1 || cost < best_cost) { best = c; best_cost = cost; }
-  }
-  return best;
-}
-
-template <class K, class... A>
-cudaError_t launch_cluster(K kernel, Resident& seen, const GatedDims& d, int groups, int round_tokens, size_t smem,
-                           cudaStream_t s, A... a) {
-  cudaError_t e = set_max_dynamic_smem((const void*)kernel, smem);
-  if (e != cudaSuccess) return e;
-  const int c = cluster_size(kernel, seen, d, groups, round_tokens, smem);
-  cudaLaunchConfig_t cfg = {};
+void set_cluster(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr, int c, int groups, size_t smem) {
   cfg.gridDim = dim3((unsigned)(groups * c));
   cfg.blockDim = dim3(32 * kWarps);
   cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)c;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)c;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, a...);
+}
+
+// CTAs per cluster, a power of two, and CTAs per SM.  The cluster size is the one with the least (rounds in a row) x (a
+// round's time).  A round of four-warp CTAs measured 0.6 us plus 0.65 us for every CTA on the fullest SM, of which four are
+// resident and the others wait (one long sequence of 2048 channels).  Clusters are placed as densely as they fit, so the
+// launch asks for as much shared memory as lets only its share fit an SM (at 4 x 2048 x 1536, 384 CTAs: 23 us with three
+// per SM, 30 us where four fitted and SMs stayed empty).  kFit: CTAs that fit at 1 .. 4 per SM by cluster size; GPCs of
+// uneven size hold fewer of the larger ones.
+struct Split {
+  int c, per_sm;
+  double cost;
+};
+Split best_split(int groups, int rounds) {
+  constexpr int kFit[5][4] = {
+      {148, 296, 444, 592}, {148, 296, 444, 592}, {132, 284, 416, 568}, {120, 264, 384, 568}, {112, 224, 336, 496}};
+  Split best{1, 1, 0};
+  for (int c = 1, i = 0; c <= kMaxCluster && (c == 1 || c < 2 * rounds); c *= 2, ++i) {
+    int k = 1;
+    while (k < 4 && (long long)groups * c > kFit[i][k - 1]) ++k;
+    const double sets = ceil_div(groups * c, kFit[i][k - 1]);
+    const double cost = sets * ceil_div(rounds, c) * (5.0 + 6.0 * k);
+    if (best.cost == 0 || cost < best.cost) best = {c, k, cost};
+  }
+  return best;
+}
+// Dynamic shared memory of which `per_sm` CTAs, and no more, fit an SM's 228 KB (1 KB of each CTA is the system's).
+size_t smem_for(int per_sm, size_t need) {
+  const size_t share = (233472 / (size_t)per_sm - 1024) / 128 * 128;
+  return share > need ? share : need;
+}
+
+// One way of laying out a scan: its kernel, the columns and tokens of a CTA's round, its shared memory.
+template <class K>
+struct Way {
+  K kernel;
+  int cols, tokens;
+  size_t smem;
+  std::atomic<int>& ready;
+};
+template <class K>
+Split split_of(const Way<K>& w, const GatedDims& d) {
+  return best_split(d.B * ceil_div(d.W, w.cols), ceil_div(d.T, w.tokens));
+}
+template <class K, class... A>
+cudaError_t launch_way(const Way<K>& w, const Split& split, const GatedDims& d, cudaStream_t s, A... a) {
+  const size_t smem = smem_for(split.per_sm, w.smem);
+  cudaError_t e = set_max_dynamic_smem((const void*)w.kernel, smem);
+  if (e == cudaSuccess && split.c > 8 && w.ready.load(std::memory_order_relaxed) == 0) {
+    e = cudaFuncSetAttribute(w.kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) w.ready.store(1, std::memory_order_relaxed);
+  }
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  const int ngrp = ceil_div(d.W, w.cols);
+  set_cluster(cfg, attr, split.c, d.B * ngrp, smem);
+  cfg.stream = s;
+  e = cudaLaunchKernelEx(&cfg, w.kernel, d.T, d.W, ngrp, d.x_stride, d.gate_stride, a...);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }
 
 template <class T, int V, int S, bool kAsync>
-cudaError_t fwd_t(const GatedDims& d, const void* x, const void* gate, const float* init, void* h, float* fin, unsigned* st,
-                  cudaStream_t s) {
-  static Resident seen;
-  const int ngrp = ceil_div(d.W, 32 * V);
-  const size_t smem = sizeof(Maps<V>) + (kAsync ? kStages * kWarps * 2 * Rows<T, V, S, kAsync>::kBytes : 0);
-  return launch_cluster(gated_scan_kernel<T, V, S, kAsync>, seen, d, d.B * ngrp, kWarps * S, smem, s, d.T, d.W, ngrp,
-                        d.x_stride, d.gate_stride, (const T*)x, (const T*)gate, init, (T*)h, fin, st);
+auto fwd_way() {
+  static std::atomic<int> ready{0};
+  auto kernel = gated_scan_kernel<T, V, S, kAsync>;
+  using R = Rows<T, V, S, kAsync>;
+  return Way<decltype(kernel)>{kernel, 32 * V, kWarps * S,
+                               sizeof(Maps<V>) + (kAsync ? (size_t)kStages * kWarps * 2 * R::kBytes : 0), ready};
 }
-
 template <class T, class G, int V, int S, bool kAsync>
-cudaError_t bwd_t(const GatedDims& d, const void* x, const void* gate, const void* h, const float* init, const void* dh,
-                  const float* dfinal, void* dx, void* dgate, float* dinit, unsigned* st, cudaStream_t s) {
-  static Resident seen;
-  const int ngrp = ceil_div(d.W, 32 * V);
-  constexpr int kWarpBytes = 3 * Rows<T, V, S, kAsync>::kBytes + Rows<G, V, S, kAsync>::kBytes;
-  const size_t smem = sizeof(Maps<V>) + (kAsync ? kStages * kWarps * kWarpBytes : 0);
-  return launch_cluster(gated_scan_bwd_kernel<T, G, V, S, kAsync>, seen, d, d.B * ngrp, kWarps * S, smem, s, d.T, d.W, ngrp,
-                        d.x_stride, d.gate_stride, (const T*)x, (const T*)gate, (const T*)h, init, (const G*)dh, dfinal,
-                        (G*)dx, (G*)dgate, dinit, st);
+auto bwd_way() {
+  static std::atomic<int> ready{0};
+  auto kernel = gated_scan_bwd_kernel<T, G, V, S, kAsync>;
+  constexpr size_t kWarpBytes = 3 * Rows<T, V, S, kAsync>::kBytes + Rows<G, V, S, kAsync>::kBytes;
+  return Way<decltype(kernel)>{kernel, 32 * V, kWarps * S,
+                               sizeof(Maps<V>) + (kAsync ? kStages * kWarps * kWarpBytes : 0), ready};
+}
+template <class K, class... A>
+cudaError_t launch(const Way<K>& w, const GatedDims& d, cudaStream_t s, A... a) {
+  return launch_way(w, split_of(w, d), d, s, a...);
 }
 
-// Rows whose 16-byte chunks are aligned in every tensor: they are copied to shared memory, some rounds deep.
+// Rows whose 16-byte chunks are aligned in every tensor: they are copied to shared memory, a round ahead.
 bool aligned_rows(const GatedDims& d) {
   const int q = d.dtype == SWIMBA_F32 ? 4 : 8;
   return d.W % q == 0 && d.x_stride % q == 0 && d.gate_stride % q == 0;
 }
 
-#ifndef SF
-#define SF 16
-#define SB 8
-#endif
 template <class T>
 cudaError_t fwd_v(const GatedDims& d, const void* x, const void* gate, const float* init, void* h, float* fin,
                   unsigned* st, cudaStream_t s) {
-  constexpr int S = sizeof(T) == 2 ? SF : SF / 2;
-  return aligned_rows(d) ? fwd_t<T, 2, S, true>(d, x, gate, init, h, fin, st, s) : fwd_t<T, 1, 16, false>(d, x, gate, init, h, fin, st, s);
+  constexpr int S = sizeof(T) == 2 ? 16 : 8;
+  if (aligned_rows(d))
+    return launch(fwd_way<T, 2, S, true>(), d, s, (const T*)x, (const T*)gate, init,
+                         (T*)h, fin, st);
+  return launch(fwd_way<T, 1, 16, false>(), d, s, (const T*)x, (const T*)gate, init, (T*)h, fin, st);
 }
 
 template <class T, class G>
 cudaError_t bwd_v(const GatedDims& d, const void* x, const void* gate, const void* h, const float* init, const void* dh,
                   const float* dfinal, void* dx, void* dgate, float* dinit, unsigned* st, cudaStream_t s) {
-  constexpr int S = sizeof(T) == 2 ? SB : SB / 2;
-  return aligned_rows(d) ? bwd_t<T, G, 2, S, true>(d, x, gate, h, init, dh, dfinal, dx, dgate, dinit, st, s)
-                         : bwd_t<T, G, 1, 8, false>(d, x, gate, h, init, dh, dfinal, dx, dgate, dinit, st, s);
+  constexpr int S = sizeof(T) == 2 ? 8 : 4;
+  auto go = [&](auto launch) {
+    return launch(d, s, (const T*)x, (const T*)gate, (const T*)h, init, (const G*)dh, dfinal, (G*)dx, (G*)dgate, dinit, st);
+  };
+  if (aligned_rows(d))
+    return go([](auto... a) { return launch(bwd_way<T, G, 2, S, true>(), a...); });
+  return go([](auto... a) { return launch(bwd_way<T, G, 1, 8, false>(), a...); });
 }
 
 template <class T>

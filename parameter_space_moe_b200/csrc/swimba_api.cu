@@ -567,8 +567,8 @@ static swimba_status make_gated_dims(const swimba_gated_dims* in, GatedDims* d) 
       !ok_grad(in->grad_dtype, in->dtype) || (in->x_stride != 0 && in->x_stride < in->width) ||
       (in->gate_stride != 0 && in->gate_stride < in->width))
     return SWIMBA_ERR_INVALID_ARG;
-  // token indexes and the scan's grid (8 CTAs for every 32 channels at most) stay within 31 bits
-  if ((long long)in->batch * in->seqlen >= (1LL << 30) || (long long)in->batch * (in->width / 32 + 1) >= (1LL << 27) ||
+  // token indexes and the scan's grid (16 CTAs for every 32 channels at most) stay within 31 bits
+  if ((long long)in->batch * in->seqlen >= (1LL << 30) || (long long)in->batch * (in->width / 32 + 1) >= (1LL << 26) ||
       in->seqlen > (1 << 29) || in->x_stride >= (1LL << 31) || in->gate_stride >= (1LL << 31))
     return SWIMBA_ERR_UNSUPPORTED;
   *d = {in->batch, in->seqlen, in->width, in->dtype, in->grad_dtype, in->x_stride ? in->x_stride : in->width,
