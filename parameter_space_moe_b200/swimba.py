@@ -264,25 +264,23 @@ def ffn_dims(rows, d_model, d_ff, dtype, activation=SILU):
     return FfnDims(rows, d_model, d_ff, dtype, activation)
 
 
+def _refuse(fn):
+    raise SwimbaError(fn, 1)
+
+
 def _dense(fn, dev, n, dtype, *tensors):
     """Pointers of dense tensors of n elements of one dtype on GPU `dev` (None passes)."""
-    out = []
-    for t in tensors:
-        if t is None:
-            out.append(None)
-            continue
-        if t.get_device() != dev or t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
-            raise SwimbaError(fn, 1)
-        out.append(t.data_ptr())
-    return out
+    return [None if t is None else t.data_ptr() if (t.get_device() == dev and t.dtype is dtype and t.numel() == n
+                                                    and t.is_contiguous()) else _refuse(fn) for t in tensors]
 
 
 def _rows(fn, dev, rows, width, stride, dtype, t):
     """Pointer of a tensor of rows x width whose rows (all leading dimensions flattened) lie `stride` apart."""
-    if t.get_device() != dev or t.dtype is not dtype or t.numel() != rows * width or t.shape[-1] != width:
+    shape = t.shape
+    if t.get_device() != dev or t.dtype is not dtype or t.numel() != rows * width or shape[-1] != width:
         raise SwimbaError(fn, 1)
-    if not t.is_contiguous() or (stride and stride != width and rows > 1):
-        step, shape = stride or width, t.shape
+    if (stride and stride != width and rows > 1) or not t.is_contiguous():
+        step = stride or width
         if width > 1 and t.stride(-1) != 1:
             raise SwimbaError(fn, 1)
         for k in range(len(shape) - 2, -1, -1):
@@ -293,7 +291,7 @@ def _rows(fn, dev, rows, width, stride, dtype, t):
 
 
 def _device(fn, t):
-    dev = t.get_device() if t is not None else -1
+    dev = -1 if t is None else t.get_device()
     if dev < 0:
         raise SwimbaError(fn, 1)
     return dev
@@ -303,12 +301,12 @@ def _run(fn, dev, stream, *args):
     """Calls the library with GPU `dev` current, on its current stream or the given one (of that GPU)."""
     if stream is None:
         s = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index != dev:
+        raise SwimbaError(fn, 1)
     else:
-        if stream.device.index != dev:
-            raise SwimbaError(fn, 1)
         s = stream.cuda_stream
     call = getattr(_lib or lib(), fn)
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         code = call(*args, s)
     else:
         with torch.cuda.device(dev):
