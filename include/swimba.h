@@ -357,7 +357,7 @@ typedef struct {
 } swimba_ffn_dims;
 
 /* Bytes of workspace of the two entry points below (0 if the dims are invalid or unsupported).  D and F must be
- * multiples of 8 (of 4 in fp32). */
+ * multiples of 8. */
 size_t swimba_gated_ffn_workspace_size(const swimba_ffn_dims* dims);
 size_t swimba_gated_ffn_bwd_workspace_size(const swimba_ffn_dims* dims);
 
@@ -366,7 +366,9 @@ size_t swimba_gated_ffn_bwd_workspace_size(const swimba_ffn_dims* dims);
  *   x [M][D]; w_gate, w_up [F][D]; w_down [D][F]
  *   gate, up [M][F] out, each or NULL (kept for the gradients); h [M][F] out; out [M][D] out
  * Products accumulate in fp32; h is formed from the fp32 values and rounded once, and the last product reads the
- * rounded h. */
+ * rounded h.  fp32 tensors are split into three bf16 tensors each, whose products keep fp32's accuracy; results that
+ * depend on an infinite input are then NaN.  A device status of SWIMBA_ERR_TIMEOUT means a bounded wait of the
+ * tensor-core kernel gave up (outputs invalid). */
 swimba_status swimba_gated_ffn(const swimba_ffn_dims* dims, const void* x, const void* w_gate, const void* w_up,
                                const void* w_down, void* gate, void* up, void* h, void* out, void* ws, size_t ws_bytes,
                                void* stream);

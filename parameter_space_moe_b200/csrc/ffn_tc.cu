@@ -12,8 +12,12 @@
 //               in shared memory (64-byte swizzle: no bank conflicts) and stores it with TMA, two blocks in flight.
 //               Stored from registers, a warp's 16-byte stores touched 32 rows each and held the epilogue of the
 //               8192 x 768 x 2048 forward to 10 us a tile, twice the tile's MMAs
+// fp32 products (six segments of bf16 planes) leave the accumulator every 1024 of K and are added up in registers: the
+// tensor cores cut what an addition shifts out, which over one chain of 12 x 2816 put the gradient of x 2.5e-5 off.
 // Persistent over the units (problem, tile, split of K); a product with few tiles is split along K into fp32
 // partial sums, added in a fixed order by a second kernel.
+#include <math.h>
+
 #include "ffn_act.cuh"
 #include "ffn_tc.cuh"
 #include "tc_common.cuh"
@@ -120,13 +124,22 @@ __device__ __forceinline__ void store_block(const CUtensorMap* map, uint8_t* sta
   }
 }
 
-// The 32 values at p as four vectors; those from `left` on (a multiple of 8), or all of a dead row, are 0.
+// The 32 values at p as vectors of 16 bytes; those from `left` on (a multiple of a vector), or all of a dead row, are 0.
 template <class T>
-__device__ __forceinline__ void load_row(const T* p, bool live, int left, uint4 (&v)[4]) {
+struct RowOf {
+  static constexpr int kPer = 16 / (int)sizeof(T), kVecs = 32 / kPer;
+  uint4 v[kVecs];
+  __device__ __forceinline__ void load(const T* p, bool live, int left) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    v[i] = live && 8 * i < left ? reinterpret_cast<const uint4*>(p)[i] : make_uint4(0u, 0u, 0u, 0u);
-}
+    for (int i = 0; i < kVecs; ++i)
+      v[i] = live && kPer * i < left ? reinterpret_cast<const uint4*>(p)[i] : make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ float get(int j) const {
+    T t[kPer];
+    memcpy(t, &v[j / kPer], 16);
+    return to_f32(t[j % kPer]);
+  }
+};
 
 template <bool kPair, int kEpi, int kAct, class T>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -134,6 +147,10 @@ ffn_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
   constexpr int TM = kPair ? 256 : 128, TN = kPair ? 256 : 128;
   constexpr int kFeat = kEpi == kFfnGlu ? TN / 2 : TN;  // output columns of a tile
   constexpr uint32_t kTmemCols = 2 * TN;
+  #ifndef KCH
+#define KCH 4
+#endif
+  constexpr int kChain = sizeof(T) == 4 ? KCH : 1 << 30;  // K blocks of one accumulation
   constexpr int kPart = kFeat / (kEpiWarps / 4);        // columns of a tile that one warp drains
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = tc::smem_u32(smem_raw);
@@ -248,8 +265,18 @@ ffn_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
       const uint32_t a_far = q.a_mn ? 4 * 2048 >> 4 : kBox >> 4, b_far = q.b_mn ? 4 * 2048 >> 4 : kBox >> 4;
       if (!tc::mbar_wait(&acc_empty[buf], acc_phase ^ 1u, abort_flag)) { ok = false; break; }
       tc::fence_after_sync();
-      const uint32_t dt = tmem + (uint32_t)(buf * TN);
+      uint32_t dt = tmem + (uint32_t)(buf * TN);
+      int begin = t.kb0;
       for (int i = t.kb0; i < t.kb1; ++i) {
+        if (i - begin == kChain) {  // the chain so far goes to the epilogue, the next one starts from zero
+          if (kPair) tc::mma_commit_pair(&acc_full[buf], 0x3);
+          else tc::mma_commit(&acc_full[buf]);
+          if (++buf == 2) { buf = 0; acc_phase ^= 1u; }
+          if (!tc::mbar_wait(&acc_empty[buf], acc_phase ^ 1u, abort_flag)) { ok = false; break; }
+          tc::fence_after_sync();
+          dt = tmem + (uint32_t)(buf * TN);
+          begin = i;
+        }
         if (!tc::mbar_wait(&full[stage], phase, abort_flag)) { ok = false; break; }
         tc::fence_after_sync();
         const uint32_t sa = tc::smem_u32(smem + stage * kStageBytes), sb = sa + 2 * kBox;
@@ -257,7 +284,7 @@ ffn_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
         const uint64_t db = q.b_mn ? tc::sdesc_mnmajor_sw128(sb, kBox) : tc::sdesc_kmajor_sw128(sb);
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk) {
-          const uint32_t acc = i > t.kb0 || kk > 0;
+          const uint32_t acc = i > begin || kk > 0;
           const uint64_t dak = da + (kk & 3) * a_step + (kk >> 2) * a_far, dbk = db + (kk & 3) * b_step + (kk >> 2) * b_far;
           if (kPair) tc::mma_f16_pair(dt, dak, dbk, idesc, acc);
           else tc::mma_f16(dt, dak, dbk, idesc, acc);
@@ -292,60 +319,56 @@ ffn_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
       const Prob& q = a.prob[t.p];
       const int mw = t.tm * TM + 128 * (int)rank + 32 * q4, m = mw + lane;
       const int n0 = t.tn * kFeat + part * kPart;
-      uint4 ng[4], nu[4];  // kFfnDglu: gate and up of the next block
+      RowOf<T> ng, nu;  // kFfnDglu: gate and up of the next block (of this one in fp32, whose registers hold no more)
+      constexpr bool kAhead = sizeof(T) == 2;
       auto fetch = [&](int c) {
         const size_t at = (size_t)m * q.N + n0 + c;
-        load_row<T>((const T*)a.in1 + at, m < q.M, q.N - n0 - c, ng);
-        load_row<T>((const T*)a.in2 + at, m < q.M, q.N - n0 - c, nu);
+        ng.load((const T*)a.in1 + at, m < q.M, q.N - n0 - c);
+        nu.load((const T*)a.in2 + at, m < q.M, q.N - n0 - c);
       };
-      if (kEpi == kFfnDglu) fetch(0);
-      if (!tc::mbar_wait(&acc_full[buf], acc_phase, abort_flag)) {
-        *abort_flag = 1;
-        atomicOr(a.st, ST_TIMEOUT);
-        break;
-      }
-      tc::fence_after_sync();
-      const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(buf * TN + part * kPart);
-#pragma unroll 1
-      for (int c = 0; c < kPart; c += 32) {
-        uint32_t ra[32], rb[32];
-        tc::tmem_ld_32x32b_x32(taddr + c, ra);
-        if (kEpi == kFfnGlu) tc::tmem_ld_32x32b_x32(taddr + TN / 2 + c, rb);
-        tc::tmem_ld_wait(ra);
-        if (kEpi == kFfnGlu) tc::tmem_ld_wait(rb);
+      if (kEpi == kFfnDglu && kAhead) fetch(0);
+      auto wait_full = [&]() {
+        if (!tc::mbar_wait(&acc_full[buf], acc_phase, abort_flag)) {
+          *abort_flag = 1;
+          atomicOr(a.st, ST_TIMEOUT);
+          return false;
+        }
+        tc::fence_after_sync();
+        return true;
+      };
+      auto free_acc = [&]() {
+        tc::fence_before_sync();
+        __syncwarp();
+        // orders only TMEM reads (the tcgen05 fence), so a pair's arrival is relaxed
+        if (lane == 0) {
+          if (kPair) tc::mbar_arrive_cluster_relaxed(acc_empty0 + 8u * (uint32_t)buf);
+          else tc::mbar_arrive(&acc_empty[buf]);
+        }
+        if (++buf == 2) { buf = 0; acc_phase ^= 1u; }
+      };
+      // What becomes of 32 columns at n0 + c: v the accumulators, w the up half's (kFfnGlu).
+      auto finish = [&](int c, float (&v)[32], float (&w)[32]) {
         const int n = n0 + c;
-        float v[32], w[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(ra[i]);
         const bool some = mw < q.M && n < q.N;  // the same in the whole warp
         if (kEpi == kFfnGlu) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) w[i] = __uint_as_float(rb[i]);
           if (some) {
             if (a.out2 >= 0) store_block<T>(&maps.o[a.out2], staged, turn, lane, v, n, mw, 0);
             if (a.out3 >= 0) store_block<T>(&maps.o[a.out3], staged, turn, lane, w, n, mw, 0);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = act_value<kAct>(v[i]) * w[i];
+            for (int i = 0; i < 32; ++i) v[i] = act_value<kAct, sizeof(T) == 4>(v[i]) * w[i];
             store_block<T>(&maps.o[q.out], staged, turn, lane, v, n, mw, 0);
           }
         } else if (kEpi == kFfnDglu) {
-          uint4 cg[4], cu[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) { cg[i] = ng[i]; cu[i] = nu[i]; }
-          if (c + 32 < kPart) fetch(c + 32);
+          if (!kAhead) fetch(c);
+          const RowOf<T> cg = ng, cu = nu;
+          if (kAhead && c + 32 < kPart) fetch(c + 32);
           if (some) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              T tg[8], tu[8];
-              memcpy(tg, &cg[i], 16);
-              memcpy(tu, &cu[i], 16);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                float slope;
-                const float act = act_both<kAct>(to_f32(tg[j]), slope);
-                w[8 * i + j] = v[8 * i + j] * act;
-                v[8 * i + j] *= to_f32(tu[j]) * slope;
-              }
+            for (int i = 0; i < 32; ++i) {
+              float slope;
+              const float act = act_both<kAct, sizeof(T) == 4>(cg.get(i), slope);
+              w[i] = v[i] * act;
+              v[i] *= cu.get(i) * slope;
             }
             store_block<T>(&maps.o[q.out], staged, turn, lane, v, n, mw, 0);
             store_block<T>(&maps.o[a.out2], staged, turn, lane, w, n, mw, 0);
@@ -354,15 +377,62 @@ ffn_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
           if (q.split > 1) store_block<float>(&maps.o[q.out], staged, turn, lane, v, n, mw, t.s);
           else store_block<T>(&maps.o[q.out], staged, turn, lane, v, n, mw, 0);
         }
+      };
+      bool ok = true;
+      if constexpr (sizeof(T) == 4) {
+        float v[kPart / 32][32], w[kEpi == kFfnGlu ? kPart / 32 : 1][32];
+#pragma unroll
+        for (int c = 0; c < kPart / 32; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[c][i] = 0.f;
+        if (kEpi == kFfnGlu) {
+#pragma unroll
+          for (int c = 0; c < kPart / 32; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[c][i] = 0.f;
+        }
+        for (int kb = t.kb0; kb < t.kb1; kb += kChain) {
+          if (!wait_full()) { ok = false; break; }
+          const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(buf * TN + part * kPart);
+#pragma unroll
+          for (int c = 0; c < kPart / 32; ++c) {
+            uint32_t r[32];
+            tc::tmem_ld_32x32b_x32(taddr + 32 * c, r);
+            tc::tmem_ld_wait(r);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[c][i] += __uint_as_float(r[i]);
+            if (kEpi == kFfnGlu) {
+              tc::tmem_ld_32x32b_x32(taddr + TN / 2 + 32 * c, r);
+              tc::tmem_ld_wait(r);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) w[c][i] += __uint_as_float(r[i]);
+            }
+          }
+          free_acc();
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < kPart / 32; ++c) finish(32 * c, v[c], w[kEpi == kFfnGlu ? c : 0]);
+      } else {
+        if (!wait_full()) break;
+        const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(buf * TN + part * kPart);
+#pragma unroll 1
+        for (int c = 0; c < kPart; c += 32) {
+          uint32_t ra[32], rb[32];
+          tc::tmem_ld_32x32b_x32(taddr + c, ra);
+          if (kEpi == kFfnGlu) tc::tmem_ld_32x32b_x32(taddr + TN / 2 + c, rb);
+          tc::tmem_ld_wait(ra);
+          if (kEpi == kFfnGlu) tc::tmem_ld_wait(rb);
+          float v[32], w[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            v[i] = __uint_as_float(ra[i]);
+            w[i] = kEpi == kFfnGlu ? __uint_as_float(rb[i]) : 0.f;
+          }
+          finish(c, v, w);
+        }
+        free_acc();
       }
-      tc::fence_before_sync();
-      __syncwarp();
-      // orders only TMEM reads (the tcgen05 fence), so a pair's arrival is relaxed
-      if (lane == 0) {
-        if (kPair) tc::mbar_arrive_cluster_relaxed(acc_empty0 + 8u * (uint32_t)buf);
-        else tc::mbar_arrive(&acc_empty[buf]);
-      }
-      if (++buf == 2) { buf = 0; acc_phase ^= 1u; }
     }
     if (lane == 0) tc::bulk_wait_all();
   }
@@ -376,9 +446,10 @@ ffn_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
   }
 }
 
-// out = sum of the split partial sums, in order; four columns per thread.
+// out = sum of the split partial sums, in order; four columns per thread.  The loads of eight splits are in flight
+// together: one after the other, 16 splits of a small product took 11 us.
 template <class T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(128)
 ffn_reduce_kernel(const __grid_constant__ Args a) {
   griddep_launch_dependents();
   griddep_wait();
@@ -388,9 +459,14 @@ ffn_reduce_kernel(const __grid_constant__ Args a) {
     const size_t n = (size_t)q.M * q.N;
     for (size_t i = 4 * ((size_t)blockIdx.x * blockDim.x + threadIdx.x); i < n; i += 4 * (size_t)gridDim.x * blockDim.x) {
       float v[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int s = 0; s < q.split; ++s) {
-        const float4 w = __ldcs(reinterpret_cast<const float4*>(q.part + s * n + i));
-        v[0] += w.x; v[1] += w.y; v[2] += w.z; v[3] += w.w;
+      for (int s0 = 0; s0 < q.split; s0 += 8) {
+        float4 w[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          if (s0 + s < q.split) w[s] = __ldcs(reinterpret_cast<const float4*>(q.part + (s0 + s) * n + i));
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          if (s0 + s < q.split) { v[0] += w[s].x; v[1] += w[s].y; v[2] += w[s].z; v[3] += w[s].w; }
       }
       store_vec<T, 4>((T*)q.dst + i, v);
     }
@@ -482,8 +558,8 @@ cudaError_t go_type(const FfnLaunch& l, const Plan& pl, const Maps& maps, const 
   size_t most = 0;
   for (int p = 0; p < a.nprob; ++p)
     if (a.prob[p].split > 1 && (size_t)a.prob[p].M * a.prob[p].N > most) most = (size_t)a.prob[p].M * a.prob[p].N;
-  const size_t want = (most / 4 + 255) / 256;
-  e = launch_dependent(ffn_reduce_kernel<T>, dim3((unsigned)(want < 8 * kSms ? want : 8 * kSms)), dim3(256), 0, s, 1, a);
+  const size_t want = (most / 4 + 127) / 128;
+  e = launch_dependent(ffn_reduce_kernel<T>, dim3((unsigned)(want < 16 * kSms ? want : 16 * kSms)), dim3(128), 0, s, 1, a);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }
@@ -500,11 +576,12 @@ cudaError_t launch_ffn_tc(const FfnLaunch& l, float* partial, unsigned* st, cuda
     if (!encode_planes(&maps.m[i], l.op[i], l.op_dtype, l.epi == kFfnGlu && !pl.pair && i > 0)) return cudaErrorInvalidValue;
   for (int p = 0; p < a.nprob; ++p) a.prob[p].part = (float*)((char*)partial + (size_t)a.prob[p].part);
   a.ab_bf16 = l.op_dtype == SWIMBA_BF16;
+  const uint32_t cols = l.dtype == SWIMBA_F32 ? 16 : 32;  // a staged block's rows are 64 bytes
   // outputs: one map per problem (of its partial sums where it is split), then the other two
   for (int p = 0; p < a.nprob; ++p) {
     const Prob& q = a.prob[p];
     const bool ok = q.split > 1 ? encode_tmap_3d_planes(&maps.o[p], q.part, SWIMBA_F32, q.N, q.M, q.split, 16, 32)
-                                : encode_tmap_3d_planes(&maps.o[p], q.dst, l.dtype, q.N, q.M, 1, 32, 32);
+                                : encode_tmap_3d_planes(&maps.o[p], q.dst, l.dtype, q.N, q.M, 1, cols, 32);
     if (!ok) return cudaErrorInvalidValue;
   }
   void* more[2] = {l.out2, l.out3};
@@ -512,12 +589,67 @@ cudaError_t launch_ffn_tc(const FfnLaunch& l, float* partial, unsigned* st, cuda
   for (int i = 0; i < 2; ++i)
     if (more[i]) {
       at[i] = kFfnMaxProblems + i;
-      if (!encode_tmap_3d_planes(&maps.o[at[i]], more[i], l.dtype, a.prob[0].N, a.prob[0].M, 1, 32, 32))
+      if (!encode_tmap_3d_planes(&maps.o[at[i]], more[i], l.dtype, a.prob[0].N, a.prob[0].M, 1, cols, 32))
         return cudaErrorInvalidValue;
     }
   a.out2 = at[0]; a.out3 = at[1]; a.in1 = l.in1; a.in2 = l.in2;
   a.st = st;
-  return l.dtype == SWIMBA_BF16 ? go_type<__nv_bfloat16>(l, pl, maps, a, s) : go_type<__half>(l, pl, maps, a, s);
+  switch (l.dtype) {
+    case SWIMBA_F32: return go_type<float>(l, pl, maps, a, s);
+    case SWIMBA_BF16: return go_type<__nv_bfloat16>(l, pl, maps, a, s);
+    default: return go_type<__half>(l, pl, maps, a, s);
+  }
 }
+
+// x = h + m + l in three bf16 planes, each the rounding of what is left: 24 bits and more.  A value that rounds past
+// bf16's largest is cut instead, and what is not finite has no rest.
+namespace {
+struct Splits {
+  int n;
+  const float* src[kFfnMaxOperands];
+  __nv_bfloat16* dst[kFfnMaxOperands];
+  long long count[kFfnMaxOperands];  // multiples of 8
+};
+__global__ void __launch_bounds__(256) ffn_split_kernel(const __grid_constant__ Splits p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  for (int k = 0; k < p.n; ++k) {
+    const long long n = p.count[k];
+    for (long long i = 8 * ((long long)blockIdx.x * blockDim.x + threadIdx.x); i < n; i += 8LL * gridDim.x * blockDim.x) {
+      float v[8], h[8], m[8], l[8];
+      load_vec<float, 8>(p.src[k] + i, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        h[j] = to_f32(__float2bfloat16_rn(v[j]));
+        if (isinf(h[j])) h[j] = __uint_as_float(__float_as_uint(v[j]) & 0xffff0000u);
+        const float r = isfinite(v[j]) ? v[j] - h[j] : 0.f;
+        m[j] = to_f32(__float2bfloat16_rn(r));
+        l[j] = r - m[j];
+      }
+      store_vec<__nv_bfloat16, 8>(p.dst[k] + i, h);
+      store_vec<__nv_bfloat16, 8>(p.dst[k] + n + i, m);
+      store_vec<__nv_bfloat16, 8>(p.dst[k] + 2 * n + i, l);
+    }
+  }
+}
+}  // namespace
+
+cudaError_t launch_ffn_split(int n, const float* const* src, void* const* dst, const long long* count, cudaStream_t s) {
+  Splits p{};
+  p.n = n;
+  long long most = 0;
+  for (int k = 0; k < n; ++k) {
+    p.src[k] = src[k];
+    p.dst[k] = (__nv_bfloat16*)dst[k];
+    p.count[k] = count[k];
+    if (count[k] > most) most = count[k];
+  }
+  const long long want = (most / 8 + 255) / 256;
+  const cudaError_t e =
+      launch_dependent(ffn_split_kernel, dim3((unsigned)(want < 8 * kSms ? want : 8 * kSms)), dim3(256), 0, s, 1, p);
+  if (e == cudaSuccess) count_launches(1);
+  return e;
+}
+
 
 }  // namespace swimba

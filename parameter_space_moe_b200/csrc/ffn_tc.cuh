@@ -44,6 +44,8 @@ struct FfnLaunch {
 
 // Bytes of partial sums that the launch needs (a function of the sizes alone).
 size_t ffn_tc_partial_bytes(const FfnLaunch& l);
+// fp32 tensors of `count` values (a multiple of 8) as three bf16 planes each, whose sum they are.
+cudaError_t launch_ffn_split(int n, const float* const* src, void* const* dst, const long long* count, cudaStream_t s);
 cudaError_t launch_ffn_tc(const FfnLaunch& l, float* partial, unsigned* st, cudaStream_t s);
 
 }  // namespace swimba

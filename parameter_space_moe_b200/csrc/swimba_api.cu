@@ -580,8 +580,7 @@ static swimba_status make_ffn_dims(const swimba_ffn_dims* in, FfnDims* d) {
   if (!in || in->rows < 1 || in->d_model < 1 || in->d_ff < 1 || !any_dtype(in->dtype) ||
       (in->activation != SWIMBA_SILU && in->activation != SWIMBA_GELU))
     return SWIMBA_ERR_INVALID_ARG;
-  const int q = in->dtype == SWIMBA_F32 ? 4 : 8;
-  if (in->d_model % q != 0 || in->d_ff % q != 0 || in->d_model > (1 << 20) || in->d_ff > (1 << 20) ||
+  if (in->d_model % 8 != 0 || in->d_ff % 8 != 0 || in->d_model > (1 << 20) || in->d_ff > (1 << 20) ||
       in->rows > (1 << 24))
     return SWIMBA_ERR_UNSUPPORTED;
   *d = {in->rows, in->d_model, in->d_ff, in->dtype, in->activation};
