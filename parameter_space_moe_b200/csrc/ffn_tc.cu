@@ -12,8 +12,9 @@
 //               in shared memory (64-byte swizzle: no bank conflicts) and stores it with TMA, two blocks in flight.
 //               Stored from registers, a warp's 16-byte stores touched 32 rows each and held the epilogue of the
 //               8192 x 768 x 2048 forward to 10 us a tile, twice the tile's MMAs
-// fp32 products (six segments of bf16 planes) leave the accumulator every 1024 of K and are added up in registers: the
-// tensor cores cut what an addition shifts out, which over one chain of 12 x 2816 put the gradient of x 2.5e-5 off.
+// fp32 products (six segments of bf16 planes) leave the accumulator every 256 of K and are added up in registers: the
+// tensor cores cut what an addition shifts out.  Over one chain of 12 x 2816 that put the gradient of x 2.5e-5 off, over
+// chains of 1024 2.0e-6, of 512 1.0e-6, of 256 5e-7 (fp32 FMAs: 1.1e-6); 256 takes 4 % longer than 512.
 // Persistent over the units (problem, tile, split of K); a product with few tiles is split along K into fp32
 // partial sums, added in a fixed order by a second kernel.
 #include <math.h>
@@ -147,10 +148,7 @@ ffn_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
   constexpr int TM = kPair ? 256 : 128, TN = kPair ? 256 : 128;
   constexpr int kFeat = kEpi == kFfnGlu ? TN / 2 : TN;  // output columns of a tile
   constexpr uint32_t kTmemCols = 2 * TN;
-  #ifndef KCH
-#define KCH 4
-#endif
-  constexpr int kChain = sizeof(T) == 4 ? KCH : 1 << 30;  // K blocks of one accumulation
+  constexpr int kChain = sizeof(T) == 4 ? 2 : 1 << 30;  // K blocks of one accumulation
   constexpr int kPart = kFeat / (kEpiWarps / 4);        // columns of a tile that one warp drains
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = tc::smem_u32(smem_raw);
@@ -486,15 +484,20 @@ Plan make_plan(const FfnLaunch& l, Args* a) {
   for (int p = 0; p < l.nprob; ++p) big += tiles(l.prob[p], 256);
   pl.pair = big >= kSms / 4;
   const int t = pl.pair ? 256 : 128, slots = pl.pair ? kSms / 2 : kSms;
-  long long total = 0;
-  for (int p = 0; p < l.nprob; ++p) total += tiles(l.prob[p], t);
+  // A launch with fewer tiles than slots is split along K into units of about the same length, as long as each has two K
+  // blocks.  (The gradients of 4756 x 128 x 264: 9 weight tiles of 38 K blocks beside 38 tiles of 6.)
+  long long total = 0, blocks = 0;
+  for (int p = 0; p < l.nprob; ++p) {
+    total += tiles(l.prob[p], t);
+    blocks += tiles(l.prob[p], t) * ceil_div(l.prob[p].K, BK) * l.prob[p].nseg;
+  }
+  const long long length = (blocks + slots - 1) / slots > 2 ? (blocks + slots - 1) / slots : 2;
   long long units = 0;
   size_t off = 0;
   for (int p = 0; p < l.nprob; ++p) {
     const FfnProblem& q = l.prob[p];
     const int kbs = ceil_div(q.K, BK), nkb = kbs * q.nseg;
-    long long split = l.epi == kFfnStore && total < slots ? slots / total : 1;
-    if (split > nkb / 2) split = nkb / 2;
+    long long split = l.epi == kFfnStore && total < slots ? nkb / length : 1;
     split = split < 1 ? 1 : split > kMaxSplit ? kMaxSplit : split;
     if (a) {
       Prob& r = a->prob[p];
