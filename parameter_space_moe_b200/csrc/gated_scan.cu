@@ -23,6 +23,9 @@ namespace swimba {
 namespace {
 
 constexpr int kWarps = 4, kStages = 2;
+// CTAs whose registers fit an SM, by the tokens of a warp's round: the long rounds take twice as many.
+constexpr int fwd_resident(int S, int lane_bytes) { return S * lane_bytes > 64 ? 2 : 4; }
+constexpr int bwd_resident(int S, int lane_bytes) { return S * lane_bytes > 32 ? 2 : 4; }
 
 // fp32 arithmetic on a lane's V columns; a pair of columns lives in one 64-bit register pair, where the two-wide
 // instructions take it.
@@ -263,7 +266,7 @@ __device__ __forceinline__ Vec<V> load_state(const float* p, size_t at, bool liv
 }
 
 template <class T, int V, int S, bool kAsync>
-__global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
+__global__ void __launch_bounds__(32 * kWarps, fwd_resident(S, V * sizeof(T)))
 gated_scan_kernel(int T_, int W, int ngrp, long long xs, long long gs, const T* __restrict__ x,
                   const T* __restrict__ gate, const float* init, T* __restrict__ h, float* final_state, unsigned* status) {
   using R = Rows<T, V, S, kAsync>;
@@ -355,7 +358,7 @@ gated_scan_kernel(int T_, int W, int ngrp, long long xs, long long gs, const T* 
 
 // Token index tau counts from the last token: t = T - 1 - tau.
 template <class T, class G, int V, int S, bool kAsync>
-__global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
+__global__ void __launch_bounds__(32 * kWarps, bwd_resident(S, V * sizeof(T)))
 gated_scan_bwd_kernel(int T_, int W, int ngrp, long long xs, long long gs, const T* __restrict__ x,
                       const T* __restrict__ gate, const T* __restrict__ h, const float* init, const G* __restrict__ dh,
                       const float* dfinal, G* __restrict__ dx, G* __restrict__ dgate, float* dinit, unsigned* status) {
@@ -487,25 +490,26 @@ void set_cluster(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr, int c, int 
   cfg.numAttrs = 1;
 }
 
-// CTAs per cluster, a power of two, and CTAs per SM.  The cluster size is the one with the least (rounds in a row) x (a
-// round's time).  A round of four-warp CTAs measured 0.6 us plus 0.65 us for every CTA on the fullest SM, of which four are
-// resident and the others wait (one long sequence of 2048 channels).  Clusters are placed as densely as they fit, so the
-// launch asks for as much shared memory as lets only its share fit an SM (at 4 x 2048 x 1536, 384 CTAs: 23 us with three
-// per SM, 30 us where four fitted and SMs stayed empty).  kFit: CTAs that fit at 1 .. 4 per SM by cluster size; GPCs of
-// uneven size hold fewer of the larger ones.
+// CTAs per cluster, a power of two, and CTAs per SM.  The cluster size is the one with the least estimated time: for every
+// set of clusters that is resident together 2.5 us and its rounds in a row, a round being a fixed part, one for every CTA
+// on the fullest SM, and 0.02 us for every CTA of the cluster (fitted to sweeps of 1 .. 16 CTAs over 1 x 32768 x 2048,
+// 4 x 2048 x 1536, 1 x 30000 x 64, 1 x 20000 x 512 and odd widths; the parts stand beside the kernels' ways below).
+// Clusters are placed as densely as they fit, so the launch asks for as much shared memory as lets only its share fit an
+// SM (at 4 x 2048 x 1536, 384 CTAs: 23 us with three per SM, 30 us where four fitted and SMs stayed empty).  kFit: CTAs
+// that fit at 1 .. 4 per SM by cluster size; GPCs of uneven size hold fewer of the larger ones.
 struct Split {
   int c, per_sm;
   double cost;
 };
-Split best_split(int groups, int rounds) {
+Split best_split(int groups, int rounds, int resident, double fixed, double each) {
   constexpr int kFit[5][4] = {
       {148, 296, 444, 592}, {148, 296, 444, 592}, {132, 284, 416, 568}, {120, 264, 384, 568}, {112, 224, 336, 496}};
   Split best{1, 1, 0};
   for (int c = 1, i = 0; c <= kMaxCluster && (c == 1 || c < 2 * rounds); c *= 2, ++i) {
     int k = 1;
-    while (k < 4 && (long long)groups * c > kFit[i][k - 1]) ++k;
+    while (k < resident && (long long)groups * c > kFit[i][k - 1]) ++k;
     const double sets = ceil_div(groups * c, kFit[i][k - 1]);
-    const double cost = sets * ceil_div(rounds, c) * (5.0 + 6.0 * k);
+    const double cost = sets * (2.5 + ceil_div(rounds, c) * (fixed + each * k + 0.02 * c));
     if (best.cost == 0 || cost < best.cost) best = {c, k, cost};
   }
   return best;
@@ -520,13 +524,14 @@ size_t smem_for(int per_sm, size_t need) {
 template <class K>
 struct Way {
   K kernel;
-  int cols, tokens;
+  int cols, tokens, resident;
+  double fixed, each;  // of a round's time
   size_t smem;
   std::atomic<int>& ready;
 };
 template <class K>
 Split split_of(const Way<K>& w, const GatedDims& d) {
-  return best_split(d.B * ceil_div(d.W, w.cols), ceil_div(d.T, w.tokens));
+  return best_split(d.B * ceil_div(d.W, w.cols), ceil_div(d.T, w.tokens), w.resident, w.fixed, w.each);
 }
 template <class K, class... A>
 cudaError_t launch_way(const Way<K>& w, const Split& split, const GatedDims& d, cudaStream_t s, A... a) {
@@ -549,23 +554,36 @@ cudaError_t launch_way(const Way<K>& w, const Split& split, const GatedDims& d, 
 
 template <class T, int V, int S, bool kAsync>
 auto fwd_way() {
+  constexpr bool kLong = fwd_resident(S, V * sizeof(T)) == 2;
+  constexpr double kFixed = V == 1 ? (sizeof(T) == 2 ? 1.5 : 0.5) : kLong ? 0.8 : 0.62;
+  constexpr double kEach = V == 1 ? (sizeof(T) == 2 ? 0.5 : 1.25) : kLong ? 1.15 : 0.6;
   static std::atomic<int> ready{0};
   auto kernel = gated_scan_kernel<T, V, S, kAsync>;
   using R = Rows<T, V, S, kAsync>;
-  return Way<decltype(kernel)>{kernel, 32 * V, kWarps * S,
+  return Way<decltype(kernel)>{kernel, 32 * V, kWarps * S, fwd_resident(S, V * sizeof(T)), kFixed, kEach,
                                sizeof(Maps<V>) + (kAsync ? (size_t)kStages * kWarps * 2 * R::kBytes : 0), ready};
 }
 template <class T, class G, int V, int S, bool kAsync>
 auto bwd_way() {
+  constexpr bool kLong = bwd_resident(S, V * sizeof(T)) == 2;
+  constexpr double kFixed = V == 1 ? 1.25 : kLong ? 1.3 : 0.95;
+  constexpr double kEach = V == 1 ? 0.45 : kLong ? 0.77 : 0.4;
   static std::atomic<int> ready{0};
   auto kernel = gated_scan_bwd_kernel<T, G, V, S, kAsync>;
   constexpr size_t kWarpBytes = 3 * Rows<T, V, S, kAsync>::kBytes + Rows<G, V, S, kAsync>::kBytes;
-  return Way<decltype(kernel)>{kernel, 32 * V, kWarps * S,
+  return Way<decltype(kernel)>{kernel, 32 * V, kWarps * S, bwd_resident(S, V * sizeof(T)), kFixed, kEach,
                                sizeof(Maps<V>) + (kAsync ? kStages * kWarps * kWarpBytes : 0), ready};
 }
 template <class K, class... A>
 cudaError_t launch(const Way<K>& w, const GatedDims& d, cudaStream_t s, A... a) {
   return launch_way(w, split_of(w, d), d, s, a...);
+}
+
+// Of two ways, the cheaper: long rounds spread a round's fixed part over twice the tokens where the columns are few.
+template <class K1, class K2, class... A>
+cudaError_t launch(const Way<K1>& w1, const Way<K2>& w2, const GatedDims& d, cudaStream_t s, A... a) {
+  const Split s1 = split_of(w1, d), s2 = split_of(w2, d);
+  return s2.cost < s1.cost ? launch_way(w2, s2, d, s, a...) : launch_way(w1, s1, d, s, a...);
 }
 
 // Rows whose 16-byte chunks are aligned in every tensor: they are copied to shared memory, a round ahead.
@@ -579,7 +597,7 @@ cudaError_t fwd_v(const GatedDims& d, const void* x, const void* gate, const flo
                   unsigned* st, cudaStream_t s) {
   constexpr int S = sizeof(T) == 2 ? 16 : 8;
   if (aligned_rows(d))
-    return launch(fwd_way<T, 2, S, true>(), d, s, (const T*)x, (const T*)gate, init,
+    return launch(fwd_way<T, 2, S, true>(), fwd_way<T, 2, 2 * S, true>(), d, s, (const T*)x, (const T*)gate, init,
                          (T*)h, fin, st);
   return launch(fwd_way<T, 1, 16, false>(), d, s, (const T*)x, (const T*)gate, init, (T*)h, fin, st);
 }
@@ -592,7 +610,7 @@ cudaError_t bwd_v(const GatedDims& d, const void* x, const void* gate, const voi
     return launch(d, s, (const T*)x, (const T*)gate, (const T*)h, init, (const G*)dh, dfinal, (G*)dx, (G*)dgate, dinit, st);
   };
   if (aligned_rows(d))
-    return go([](auto... a) { return launch(bwd_way<T, G, 2, S, true>(), a...); });
+    return go([](auto... a) { return launch(bwd_way<T, G, 2, S, true>(), bwd_way<T, G, 2, 2 * S, true>(), a...); });
   return go([](auto... a) { return launch(bwd_way<T, G, 1, 8, false>(), a...); });
 }
 
