@@ -19,14 +19,16 @@ namespace {
 // as many teams as its threads allow.  Sums over a warp and addresses cost the same for few columns a thread as for many;
 // more threads hide more latency.  Columns of a thread, at most (M x D, dtype / gradients' dtype, measured):
 //   forward            16   32768 x 2048 bf16 with the residual sum: 88 us; 24 columns 102 us
-//   16-bit gradients   16   8192 x 768 bf16 / f32: 25 us; 8 columns 27 us, 24 columns 28 us
+//   16-bit gradients   16   8192 x 768 bf16 / f32 (12 columns): 27 us; 8 columns 32 us.  20000 x 2048 bf16 (16 columns,
+//                           one block of 384 threads an SM, whose registers do not spill): 103 us; two of 256 110 us
 //   f32 gradients       8   5000 x 1500: 35 us with the rows ahead in shared memory; 16 in registers 45 us
 //   odd widths          4   4099 x 1001 f32: 22 us; 8 columns 38 us, 16 columns 62 us
 // 8 where there are few rows, and 16, 24 or, in blocks of 512 threads, 32 where a block would not hold the row otherwise.
 constexpr int kMaxThreads = 512;
 constexpr int threads_of(bool wide) { return wide ? kMaxThreads : 256; }
 constexpr int kFwdBlocks = 3;  // of 256 threads, on an SM
-constexpr int bwd_blocks(int cols, bool async) { return async ? (cols <= 8 ? 4 : cols <= 16 ? 3 : 2) : cols <= 8 ? 3 : 2; }
+constexpr int bwd_blocks(int cols, bool async) { return async ? (cols <= 8 ? 4 : cols <= 16 ? 3 : 2) : cols <= 8 ? 3 : cols <= 12 ? 2 : 1; }
+constexpr int bwd_threads(int cols, bool async, bool wide) { return wide ? kMaxThreads : !async && cols > 12 ? 384 : 256; }
 constexpr int bwd_cols(int vec, bool async) { return vec == 1 ? 4 : async ? 8 : 16; }
 
 // Sums go through shared memory where a team has several warps: `red` holds two copies, used in turn, so that one barrier
@@ -233,7 +235,7 @@ struct Ahead {
 // Gradients of the block's rows.  A thread keeps its columns' sums of dy xhat and dy over all of them; the teams' sums
 // meet in shared memory and go to part[blockIdx.x][2][D] when `part` is given.
 template <class T, class G, int VEC, int NV, bool kWide, bool kAsync>
-__global__ void __launch_bounds__(threads_of(kWide), kWide ? 1 : bwd_blocks(NV* VEC, kAsync))
+__global__ void __launch_bounds__(bwd_threads(NV* VEC, kAsync, kWide), kWide ? 1 : bwd_blocks(NV* VEC, kAsync))
 layer_norm_bwd_kernel(int M, int D, int team, float eps, const T* __restrict__ r, const float* __restrict__ gamma,
                       const G* dy, const G* dr, G* dx, float* __restrict__ part) {
   __shared__ float2 red[2][kMaxThreads / 32];
@@ -434,7 +436,8 @@ Shape shape_of(int M, int D, int vec, int most, bool bwd, bool async) {
     s.team = 32 * ceil_div(n, 32 * s.nv);
   }
   // as many teams as a block takes, as long as every SM has rows for them
-  while ((s.groups + 1) * s.team <= threads_of(s.wide) && (long long)(s.groups + 1) * 148 <= M) ++s.groups;
+  const int threads = bwd ? bwd_threads(s.nv * vec, async, s.wide) : threads_of(s.wide);
+  while ((s.groups + 1) * s.team <= threads && (long long)(s.groups + 1) * 148 <= M) ++s.groups;
   const int want = ceil_div(M, s.groups), cap = 148 * (s.wide ? 1 : bwd ? bwd_blocks(s.nv * vec, async) : kFwdBlocks);
   s.blocks = want < cap ? want : cap;
   return s;
