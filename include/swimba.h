@@ -285,7 +285,7 @@ swimba_status swimba_out_proj(const swimba_dims* dims, const void* y, const void
  *    outputs and workspaces do not, and every call can be captured into a CUDA graph. */
 
 typedef struct {
-  int32_t rows;       /* M */
+  int32_t rows;       /* M: up to 2^30 */
   int32_t width;      /* D: 1 .. 16384 */
   int32_t dtype;      /* x, residual, r and y */
   int32_t grad_dtype; /* dy, dr and dx */

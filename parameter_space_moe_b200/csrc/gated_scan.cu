@@ -527,7 +527,7 @@ struct Way {
   int cols, tokens, resident;
   double fixed, each;  // of a round's time
   size_t smem;
-  std::atomic<int>& ready;
+  std::atomic<unsigned long long>& wide;  // devices (bits) on which clusters of more than 8 CTAs are allowed
 };
 template <class K>
 Split split_of(const Way<K>& w, const GatedDims& d) {
@@ -537,9 +537,14 @@ template <class K, class... A>
 cudaError_t launch_way(const Way<K>& w, const Split& split, const GatedDims& d, cudaStream_t s, A... a) {
   const size_t smem = smem_for(split.per_sm, w.smem);
   cudaError_t e = set_max_dynamic_smem((const void*)w.kernel, smem);
-  if (e == cudaSuccess && split.c > 8 && w.ready.load(std::memory_order_relaxed) == 0) {
-    e = cudaFuncSetAttribute(w.kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess) w.ready.store(1, std::memory_order_relaxed);
+  if (e == cudaSuccess && split.c > 8) {
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    const unsigned long long bit = 1ULL << (dev & 63);
+    if (e == cudaSuccess && !(w.wide.load(std::memory_order_relaxed) & bit)) {
+      e = cudaFuncSetAttribute(w.kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e == cudaSuccess) w.wide.fetch_or(bit, std::memory_order_relaxed);
+    }
   }
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -557,22 +562,22 @@ auto fwd_way() {
   constexpr bool kLong = fwd_resident(S, V * sizeof(T)) == 2;
   constexpr double kFixed = V == 1 ? (sizeof(T) == 2 ? 1.5 : 0.5) : kLong ? 0.8 : 0.62;
   constexpr double kEach = V == 1 ? (sizeof(T) == 2 ? 0.5 : 1.25) : kLong ? 1.15 : 0.6;
-  static std::atomic<int> ready{0};
+  static std::atomic<unsigned long long> wide{0};
   auto kernel = gated_scan_kernel<T, V, S, kAsync>;
   using R = Rows<T, V, S, kAsync>;
   return Way<decltype(kernel)>{kernel, 32 * V, kWarps * S, fwd_resident(S, V * sizeof(T)), kFixed, kEach,
-                               sizeof(Maps<V>) + (kAsync ? (size_t)kStages * kWarps * 2 * R::kBytes : 0), ready};
+                               sizeof(Maps<V>) + (kAsync ? (size_t)kStages * kWarps * 2 * R::kBytes : 0), wide};
 }
 template <class T, class G, int V, int S, bool kAsync>
 auto bwd_way() {
   constexpr bool kLong = bwd_resident(S, V * sizeof(T)) == 2;
   constexpr double kFixed = V == 1 ? 1.25 : kLong ? 1.3 : 0.95;
   constexpr double kEach = V == 1 ? 0.45 : kLong ? 0.77 : 0.4;
-  static std::atomic<int> ready{0};
+  static std::atomic<unsigned long long> wide{0};
   auto kernel = gated_scan_bwd_kernel<T, G, V, S, kAsync>;
   constexpr size_t kWarpBytes = 3 * Rows<T, V, S, kAsync>::kBytes + Rows<G, V, S, kAsync>::kBytes;
   return Way<decltype(kernel)>{kernel, 32 * V, kWarps * S, bwd_resident(S, V * sizeof(T)), kFixed, kEach,
-                               sizeof(Maps<V>) + (kAsync ? kStages * kWarps * kWarpBytes : 0), ready};
+                               sizeof(Maps<V>) + (kAsync ? kStages * kWarps * kWarpBytes : 0), wide};
 }
 template <class K, class... A>
 cudaError_t launch(const Way<K>& w, const GatedDims& d, cudaStream_t s, A... a) {

@@ -40,12 +40,16 @@ cudaError_t set_max_dynamic_smem(const void* kernel, size_t bytes) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> lk(mu);
-  size_t& g = granted[{dev, kernel}];
-  if (bytes <= g) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess) g = bytes;
-  return e;
+  try {
+    std::lock_guard<std::mutex> lk(mu);
+    size_t& g = granted[{dev, kernel}];
+    if (bytes <= g) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) g = bytes;
+    return e;
+  } catch (...) {  // the map could not grow: no exception leaves the C entry points
+    return cudaErrorMemoryAllocation;
+  }
 }
 
 struct Profiler {
@@ -557,7 +561,8 @@ static swimba_status make_norm_dims(const swimba_norm_dims* in, NormDims* d) {
   if (!in || in->rows < 1 || in->width < 1 || !any_dtype(in->dtype) || !ok_grad(in->grad_dtype, in->dtype) ||
       !(in->eps > 0.f) || in->eps > 3.4e38f || (in->x_stride != 0 && in->x_stride < in->width))
     return SWIMBA_ERR_INVALID_ARG;
-  if (in->width > 16384 || in->x_stride >= (1LL << 31)) return SWIMBA_ERR_UNSUPPORTED;
+  // row indexes a step behind the last row stay within 31 bits
+  if (in->width > 16384 || in->rows > (1 << 30) || in->x_stride >= (1LL << 31)) return SWIMBA_ERR_UNSUPPORTED;
   *d = {in->rows, in->width, in->dtype, in->grad_dtype, in->x_stride ? in->x_stride : in->width, in->eps};
   return SWIMBA_OK;
 }
@@ -580,8 +585,10 @@ static swimba_status make_ffn_dims(const swimba_ffn_dims* in, FfnDims* d) {
   if (!in || in->rows < 1 || in->d_model < 1 || in->d_ff < 1 || !any_dtype(in->dtype) ||
       (in->activation != SWIMBA_SILU && in->activation != SWIMBA_GELU))
     return SWIMBA_ERR_INVALID_ARG;
-  if (in->d_model % 8 != 0 || in->d_ff % 8 != 0 || in->d_model > (1 << 20) || in->d_ff > (1 << 20) ||
-      in->rows > (1 << 24))
+  // tiles of 128 x 64 outputs at least, four products of them, are counted in 31 bits
+  const long long wide = in->d_model > in->d_ff ? in->d_model : in->d_ff;
+  if (in->d_model % 8 != 0 || in->d_ff % 8 != 0 || wide > (1 << 20) || in->rows > (1 << 24) ||
+      in->rows * wide > (1LL << 38) || wide * in->d_model > (1LL << 38) || wide * in->d_ff > (1LL << 38))
     return SWIMBA_ERR_UNSUPPORTED;
   *d = {in->rows, in->d_model, in->d_ff, in->dtype, in->activation};
   return SWIMBA_OK;

@@ -91,6 +91,7 @@ def test_pointers(L, name):
                                        dict(eps=math.nan), dict(eps=math.inf), dict(x_stride=63),
                                        dict(x_stride=-64))],
     ("layer_norm", dict(width=16385), 2), ("layer_norm", dict(x_stride=1 << 31), 2),
+    ("layer_norm", dict(rows=(1 << 30) + 1), 2),
     *[("gated_scan", kw, 1) for kw in (dict(batch=0), dict(seqlen=0), dict(seqlen=-5), dict(width=0), dict(dtype=7),
                                        dict(grad_dtype=swimba.F16), dict(x_stride=1), dict(gate_stride=63))],
     ("gated_scan", dict(batch=1 << 20, seqlen=1 << 20), 2), ("gated_scan", dict(batch=1 << 20, width=1 << 14), 2),
@@ -98,7 +99,9 @@ def test_pointers(L, name):
     *[("gated_ffn", kw, 1) for kw in (dict(rows=0), dict(d_model=0), dict(d_ff=-8), dict(dtype=5),
                                       dict(activation=2), dict(activation=-1))],
     *[("gated_ffn", kw, 2) for kw in (dict(d_model=60), dict(d_ff=132), dict(dtype=swimba.F32, d_ff=126),
-                                      dict(d_ff=(1 << 20) + 8), dict(rows=(1 << 24) + 1))],
+                                      dict(d_ff=(1 << 20) + 8), dict(rows=(1 << 24) + 1),
+                                      dict(dtype=swimba.F32, d_model=68), dict(rows=1 << 24, d_ff=1 << 20),
+                                      dict(d_model=1 << 20, d_ff=1 << 20))],
 ])
 def test_dims(L, name, kw, code):
     d = OPS[name](**kw)
@@ -116,6 +119,14 @@ def test_workspace_sizes(L):
     assert small <= large == swimba.layer_norm_bwd_workspace_size(norm(rows=1 << 21, width=768))
     assert swimba.gated_ffn_bwd_workspace_size(ffn()) >= 2 * 8 * 128 * 2
     assert swimba.gated_ffn_workspace_size(ffn()) > 0
+
+
+def test_fp32_workspaces_hold_the_planes(L):
+    """fp32 tensors of the block are split into three bf16 planes in the workspace: 6 bytes a value."""
+    M, D, F = 100, 64, 128
+    d = ffn(rows=M, dtype=swimba.F32)
+    assert swimba.gated_ffn_workspace_size(d) >= 6 * (M * D + 3 * F * D + M * F)
+    assert swimba.gated_ffn_bwd_workspace_size(d) >= 8 * M * F + 6 * (2 * M * D + 3 * F * D + 3 * M * F)
 
 
 def test_the_binding_refuses_tensors_off_the_gpu():

@@ -86,7 +86,9 @@ def norm_bound(r, gamma, beta, eps):
 
 
 NORM_SHAPES = [(1, 1), (3, 8), (5, 33), (2, 64), (7, 255), (4, 768), (300, 768), (3, 1000), (2, 1001), (9, 2048), (2, 4096),
-               (3, 5003), (2, 8192), (2, 8200), (2, 16384), (1, 16383)]
+               (3, 5003), (2, 8192), (2, 8200), (2, 16384), (1, 16383),
+               # enough rows for the layouts with more columns a thread, and columns that fill no layout
+               (700, 2048), (600, 1001), (3, 5000), (601, 520)]
 
 
 @pytest.mark.parametrize("dt", TYPES)
@@ -219,7 +221,9 @@ def scan_bound(a, values, da, b_err, scale):
 
 
 SCAN_SHAPES = [(1, 1, 1), (2, 1, 64), (3, 5, 7), (1, 64, 32), (2, 65, 66), (1, 63, 33), (1, 700, 200), (4, 513, 96), (3, 1111, 333),
-               (1, 2100, 2), (70, 3, 128), (1, 4097, 65), (2, 600, 1536)]
+               (1, 2100, 2), (70, 3, 128), (1, 4097, 65), (2, 600, 1536),
+               # few columns and many tokens: the largest clusters and the long rounds
+               (1, 9001, 64), (3, 2500, 256), (1, 300, 4096)]
 
 
 def scan_inputs(rng, B, T, W, t, cut):
@@ -632,3 +636,52 @@ def test_the_binding_checks_its_tensors():
             swimba.gated_ffn(f, x, w, w, w, None, None, x, x, ws[:n] if n else None)
         assert e.value.code == 4
     ok()
+
+
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^31 elements: the last rows and tokens come out like a small call's on the same values."""
+    D, M = 8192, 270000
+    x = torch.zeros(M, D, dtype=torch.bfloat16, device="cuda")
+    x[-4:] = torch.randn(4, D, device="cuda").bfloat16()
+    y = torch.empty_like(x)
+    swimba.layer_norm(swimba.norm_dims(M, D, swimba.BF16), x, None, None, None, y, None)
+    ok()
+    tail = x[-4:].double().cpu().numpy()
+    within(y[-4:].double().cpu().numpy(), O.layer_norm(tail, None, None, None, float(np.float32(1e-5)))[0],
+           norm_bound(tail, None, None, 1e-5), torch.bfloat16, "tail rows")
+    assert float(y[:-4].float().abs().max()) == 0.0
+    d = swimba.norm_dims(M, D, swimba.BF16)
+    ws = torch.empty(swimba.layer_norm_bwd_workspace_size(d), dtype=torch.uint8, device="cuda")
+    dy = torch.zeros_like(x)
+    dy[-4:] = torch.randn(4, D, device="cuda").bfloat16()
+    dg = torch.empty(D, device="cuda")
+    swimba.layer_norm_bwd(d, x, None, dy, None, y, dg, None, ws)
+    ok()
+    dyn = dy[-4:].double().cpu().numpy()
+    dx, dgn, _ = O.layer_norm_bwd(tail, None, dyn, None, float(np.float32(1e-5)))
+    bx, bg, _ = norm_bwd_bounds(tail, None, dyn, None, 1e-5)
+    within(y[-4:].double().cpu().numpy(), dx, bx, torch.bfloat16, "tail gradients")
+    within(dg.double().cpu().numpy(), dgn, bg, torch.float32, "dgamma")
+    # one sequence of 2^31 + values as the recurrence: the last tokens, behind a closed gate, know nothing of the others
+    B, T, W = 1, 540000, 4096
+    gate = x.view(B, T, W)
+    gate.zero_()
+    gate[0, T - 40] = -float("inf")
+    src = dy.view(B, T, W)
+    src[0, -41:] = torch.randn(41, W, device="cuda").bfloat16()
+    src[0, :-41] = 3.0
+    out, fin = y.view(B, T, W), torch.empty(B, W, device="cuda")
+    swimba.gated_scan(swimba.gated_dims(B, T, W, swimba.BF16), src, gate, None, out, fin)
+    ok()
+    want = torch.empty(B, 40, W, dtype=torch.bfloat16, device="cuda")
+    last = torch.empty(B, W, device="cuda")
+    swimba.gated_scan(swimba.gated_dims(B, 40, W, swimba.BF16), src[:, -40:].contiguous(), gate[:, -40:].contiguous(), None,
+                      want, last)
+    ok()
+    # gates of 1/2 forget within 40 tokens; both sides' fp32 values are off by 8 u of the largest x a step, summed by the
+    # gates to twice that, and h is rounded once on either side
+    big = float(src[0, -40:].float().abs().max())
+    assert float((fin - last).abs().max()) <= 2 * 2 * 8 * U * big
+    a, b = out[:, -40:].double(), want.double()
+    assert bool(((a - b).abs() <= 2 * half(torch.bfloat16) * b.abs() + 32 * U * big).all())
+    assert bool((out[0, 1000:2000].float() == 3.0).all())
