@@ -15,6 +15,11 @@
 // fp32 products (six segments of bf16 planes) leave the accumulator every 256 of K and are added up in registers: the
 // tensor cores cut what an addition shifts out.  Over one chain of 12 x 2816 that put the gradient of x 2.5e-5 off, over
 // chains of 1024 2.0e-6, of 512 1.0e-6, of 256 5e-7 (fp32 FMAs: 1.1e-6); 256 takes 4 % longer than 512.
+// Bounds, bf16.  Many rows: the tensor pipe under the power cap (8192 x 2048 x 5632, the gradients of x and the weights:
+// 640 us, pipe 87 % active at the 1.43 GHz that the cap leaves), the epilogue's loads and stores where a tile's K is short
+// (gate and up at K = 768: 46 us, pipe 56 %; dgate and dup with their two more inputs: 159 us, 63 %), and
+// turns that do not fill the SMs (8192 x 768 from K = 2048: 96 tiles on 74 pairs, 30.7 us, 41 %).  256 rows: the weights'
+// bytes and each launch's start and end (256 x 2048 x 5632, 74 MB: 21 + 14 + 5 us alone, 32 us together).
 // Persistent over the units (problem, tile, split of K); a product with few tiles is split along K into fp32
 // partial sums, added in a fixed order by a second kernel.
 #include <math.h>

@@ -13,6 +13,12 @@
 // cluster barrier would first wait for the round's stores of h), and every warp then replays its tokens from its true
 // carried value.  So each input is read once, the split along time needs no pass over memory, no workspace and no
 // waiting between clusters, and sums run in a fixed order.  All in fp32, pairs of columns by two-wide instructions.
+//
+// Bounds.  Not HBM alone: a round is loads, maps, the exchange across the cluster and the replay, and the registers that
+// hold its tokens leave 8 to 16 warps an SM to hide one behind another.  bf16: 1 x 32768 x 2048 (403 MB) 104 us, 0.59 of a
+// copy's rate with 42 % of the issue slots used (21 instructions an element); 4 x 2048 x 1536 (75 MB) 23 us; its gradients
+// (151 MB) 38 us.  The step reads and writes the state once: 256 x 4096 bf16, 3.6 us on the GPU with state and rows in L2,
+// 6.0 us from HBM.
 #include <atomic>
 
 #include "block_common.cuh"

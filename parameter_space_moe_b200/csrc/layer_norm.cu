@@ -8,7 +8,12 @@
 // Both passes read each row once into registers and take the mean first and the centred squares second, so
 // no difference of large sums is formed.  Everything between the loads and the stores is fp32; y is
 // normalised from the fp32 sum, not from the rounded r.  The backward pass takes the statistics again from
-// the stored r: two more sums per row cost nothing next to the row's bytes, and no statistics are kept.
+// the stored r, so that no caller has to keep them.
+//
+// Bounds.  Forward: HBM (32768 x 2048 bf16 with the residual sum, 537 MB: 88 us, 0.93 of a copy's rate).  Gradients:
+// instructions and the latency of a row's four sums, with the columns' sums holding 128 registers a thread (8192 x 768
+// bf16 / f32, 88 MB: 24 us and 5 us for the partial sums, half of a copy's rate; an issue slot in two is used).
+// Few rows: one launch's latency (256 x 2048: 3.2 us on the GPU).
 #include "block_common.cuh"
 
 namespace swimba {
