@@ -12,7 +12,7 @@
 //
 // Bounds.  Forward: HBM (32768 x 2048 bf16 with the residual sum, 537 MB: 88 us, 0.93 of a copy's rate).  Gradients:
 // instructions and the latency of a row's four sums, with the columns' sums holding 128 registers a thread (8192 x 768
-// bf16 / f32, 88 MB: 24 us and 5 us for the partial sums, half of a copy's rate; an issue slot in two is used).
+// bf16 / f32, 88 MB: 25 us with the partial sums' launch, 0.54 of a copy's rate).
 // Few rows: one launch's latency (256 x 2048: 3.2 us on the GPU).
 #include "block_common.cuh"
 
@@ -24,8 +24,8 @@ namespace {
 // as many teams as its threads allow.  Sums over a warp and addresses cost the same for few columns a thread as for many;
 // more threads hide more latency.  Columns of a thread, at most (M x D, dtype / gradients' dtype, measured):
 //   forward            16   32768 x 2048 bf16 with the residual sum: 88 us; 24 columns 102 us
-//   16-bit gradients   16   8192 x 768 bf16 / f32 (12 columns): 27 us; 8 columns 32 us.  20000 x 2048 bf16 (16 columns,
-//                           one block of 384 threads an SM, whose registers do not spill): 103 us; two of 256 110 us
+//   16-bit gradients   16   8192 x 768 bf16 / f32 (12 columns): 25 us; 8 columns 32 us.  20000 x 2048 bf16 (16 columns,
+//                           one block of 384 threads an SM, whose registers do not spill): 94 us; two of 256 96 us
 //   f32 gradients       8   5000 x 1500: 35 us with the rows ahead in shared memory; 16 in registers 45 us
 //   odd widths          4   4099 x 1001 f32: 22 us; 8 columns 38 us, 16 columns 62 us
 // 8 where there are few rows, and 16, 24 or, in blocks of 512 threads, 32 where a block would not hold the row otherwise.
@@ -238,8 +238,10 @@ struct Ahead {
 };
 
 // Gradients of the block's rows.  A thread keeps its columns' sums of dy xhat and dy over all of them; the teams' sums
-// meet in shared memory and go to part[blockIdx.x][2][D] when `part` is given.
-template <class T, class G, int VEC, int NV, bool kWide, bool kAsync>
+// meet in shared memory and go to part[blockIdx.x][2][D] when `part` is given.  kAll: every vector of every thread holds
+// columns and gamma is given, so that nothing is tested or set to 0 or 1 on the way: 16 columns (20000 x 2048 bf16: 101 -> 92 us), since with fewer the
+// compiler spills what it no longer tests (256 x 2048 bf16, 8 columns: 10.8 -> 11.4 us; 8192 x 768 f32: 25.8 -> 30.8 us).
+template <class T, class G, int VEC, int NV, bool kWide, bool kAsync, bool kAll>
 __global__ void __launch_bounds__(bwd_threads(NV* VEC, kAsync, kWide), kWide ? 1 : bwd_blocks(NV* VEC, kAsync))
 layer_norm_bwd_kernel(int M, int D, int team, float eps, const T* __restrict__ r, const float* __restrict__ gamma,
                       const G* dy, const G* dr, G* dx, float* __restrict__ part) {
@@ -249,7 +251,7 @@ layer_norm_bwd_kernel(int M, int D, int team, float eps, const T* __restrict__ r
   Team k(team, red);
   const int groups = blockDim.x / team, step = gridDim.x * groups;
   const int c0 = k.lane * VEC, gap = team * VEC;                   // this thread's columns: c0, c0 + gap, ...
-  const int live = c0 < D ? ((D - c0) / VEC + team - 1) / team : 0;  // vectors of them
+  const int live = kAll ? NV : c0 < D ? ((D - c0) / VEC + team - 1) / team : 0;  // vectors of them
   const float inv = 1.f / D;
   Ahead<T, VEC, NV, kAsync> ar;
   Ahead<G, VEC, NV, kAsync> ad, as;
@@ -263,13 +265,13 @@ layer_norm_bwd_kernel(int M, int D, int team, float eps, const T* __restrict__ r
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < VEC; ++j) ag[i][j] = ab[i][j] = 0.f;
-  // gamma stays in registers where a thread has few columns
-  constexpr bool kKeep = NV * VEC <= 8;
+  // gamma stays in registers where a thread has few columns (8192 x 768 bf16 / f32, 12 columns: 26 -> 22.7 us)
+  constexpr bool kKeep = NV * VEC <= (kAsync ? 8 : 12);
   float kept[kKeep ? NV : 1][VEC];
   auto load_gamma = [&](int i, float (&g)[VEC]) {
 #pragma unroll
     for (int j = 0; j < VEC; ++j) g[j] = 1.f;
-    if (gamma && i < live) load_vec<float, VEC>(gamma + c0 + i * gap, g);
+    if ((kAll || gamma) && i < live) load_vec<float, VEC>(gamma + c0 + i * gap, g);
   };
   if constexpr (kKeep) {
 #pragma unroll
@@ -506,7 +508,12 @@ cudaError_t bwd_t(const NormDims& d, const void* r, const float* gamma, const vo
   constexpr bool kAsync = sizeof(T) == 4 && VEC > 1;
   cudaError_t e = cudaSuccess;
   with_shape<VEC>(sh, [&](auto nv, auto wide) {
-    auto kernel = layer_norm_bwd_kernel<T, G, VEC, decltype(nv)::value, decltype(wide)::value, kAsync>;
+    constexpr int kNv = decltype(nv)::value;
+    constexpr bool kWide = decltype(wide)::value;
+    auto kernel = layer_norm_bwd_kernel<T, G, VEC, kNv, kWide, kAsync, false>;
+    if constexpr (VEC > 1 && kNv * VEC == 16 && !kAsync && !kWide) {
+      if (gamma && sh.nv * VEC * sh.team == d.D) kernel = layer_norm_bwd_kernel<T, G, VEC, kNv, kWide, kAsync, true>;
+    }
     const size_t rows = kAsync ? (size_t)sh.groups * sh.nv * sh.team * VEC * (sizeof(T) + 2 * sizeof(G)) : 0;
     const size_t sums = sh.groups > 1 ? (size_t)sh.groups * 2 * d.D * 4 : 0, smem = rows > sums ? rows : sums;
     if (smem > 40 * 1024) e = set_max_dynamic_smem((const void*)kernel, smem);
