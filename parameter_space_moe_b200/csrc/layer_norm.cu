@@ -27,14 +27,14 @@ namespace {
 //   16-bit gradients   16   8192 x 768 bf16 / f32 (12 columns): 25 us; 8 columns 32 us.  20000 x 2048 bf16 (16 columns,
 //                           one block of 384 threads an SM, whose registers do not spill): 94 us; two of 256 96 us
 //   f32 gradients       8   5000 x 1500: 35 us with the rows ahead in shared memory; 16 in registers 45 us
-//   odd widths          4   4099 x 1001 f32: 22 us; 8 columns 38 us, 16 columns 62 us
+//   odd widths          8   4099 x 1001 f32: 18 us with two blocks an SM; 4 columns 22 us, 8 with three (spills) 38 us
 // 8 where there are few rows, and 16, 24 or, in blocks of 512 threads, 32 where a block would not hold the row otherwise.
 constexpr int kMaxThreads = 512;
 constexpr int threads_of(bool wide) { return wide ? kMaxThreads : 256; }
 constexpr int kFwdBlocks = 3;  // of 256 threads, on an SM
-constexpr int bwd_blocks(int cols, bool async) { return async ? (cols <= 8 ? 4 : cols <= 16 ? 3 : 2) : cols <= 8 ? 3 : cols <= 12 ? 2 : 1; }
+constexpr int bwd_blocks(int cols, bool async) { return async ? (cols <= 8 ? 4 : cols <= 16 ? 3 : 2) : cols <= 12 ? 2 : 1; }
 constexpr int bwd_threads(int cols, bool async, bool wide) { return wide ? kMaxThreads : !async && cols > 12 ? 384 : 256; }
-constexpr int bwd_cols(int vec, bool async) { return vec == 1 ? 4 : async ? 8 : 16; }
+constexpr int bwd_cols(int vec, bool async) { return vec == 1 ? 8 : async ? 8 : 16; }
 
 // Sums go through shared memory where a team has several warps: `red` holds two copies, used in turn, so that one barrier
 // of the team per sum is enough.
@@ -238,9 +238,10 @@ struct Ahead {
 };
 
 // Gradients of the block's rows.  A thread keeps its columns' sums of dy xhat and dy over all of them; the teams' sums
-// meet in shared memory and go to part[blockIdx.x][2][D] when `part` is given.  kAll: every vector of every thread holds
-// columns and gamma is given, so that nothing is tested or set to 0 or 1 on the way: 16 columns (20000 x 2048 bf16: 101 -> 92 us), since with fewer the
-// compiler spills what it no longer tests (256 x 2048 bf16, 8 columns: 10.8 -> 11.4 us; 8192 x 768 f32: 25.8 -> 30.8 us).
+// meet in shared memory and go to part[blockIdx.x][2][D] when `part` is given.  kAll: gamma is given, and every vector of every
+// thread holds columns, of single columns every one but a thread's last, so that nothing is tested or set to 0 or 1 on the
+// way.  16 columns in vectors (20000 x 2048 bf16: 101 -> 92 us) and 8 single ones (20000 x 1001 bf16: 74 -> 64 us); with
+// others the compiler spills what it no longer tests (8192 x 768 f32: 25.8 -> 30.8 us).
 template <class T, class G, int VEC, int NV, bool kWide, bool kAsync, bool kAll>
 __global__ void __launch_bounds__(bwd_threads(NV* VEC, kAsync, kWide), kWide ? 1 : bwd_blocks(NV* VEC, kAsync))
 layer_norm_bwd_kernel(int M, int D, int team, float eps, const T* __restrict__ r, const float* __restrict__ gamma,
@@ -251,7 +252,8 @@ layer_norm_bwd_kernel(int M, int D, int team, float eps, const T* __restrict__ r
   Team k(team, red);
   const int groups = blockDim.x / team, step = gridDim.x * groups;
   const int c0 = k.lane * VEC, gap = team * VEC;                   // this thread's columns: c0, c0 + gap, ...
-  const int live = kAll ? NV : c0 < D ? ((D - c0) / VEC + team - 1) / team : 0;  // vectors of them
+  constexpr int kSure = kAll ? (VEC == 1 ? NV - 1 : NV) : 0;
+  const int live = kSure == NV ? NV : c0 < D ? ((D - c0) / VEC + team - 1) / team : 0;  // vectors of them
   const float inv = 1.f / D;
   Ahead<T, VEC, NV, kAsync> ar;
   Ahead<G, VEC, NV, kAsync> ad, as;
@@ -271,7 +273,7 @@ layer_norm_bwd_kernel(int M, int D, int team, float eps, const T* __restrict__ r
   auto load_gamma = [&](int i, float (&g)[VEC]) {
 #pragma unroll
     for (int j = 0; j < VEC; ++j) g[j] = 1.f;
-    if ((kAll || gamma) && i < live) load_vec<float, VEC>(gamma + c0 + i * gap, g);
+    if ((kAll || gamma) && (i < kSure || i < live)) load_vec<float, VEC>(gamma + c0 + i * gap, g);
   };
   if constexpr (kKeep) {
 #pragma unroll
@@ -315,7 +317,7 @@ layer_norm_bwd_kernel(int M, int D, int team, float eps, const T* __restrict__ r
       get_gamma(i, gm);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) v[i][j] = d[i][j] = 0.f;
-      if (i < live) {
+      if (i < kSure || i < live) {
         ar.get(i, v[i]);
         ad.get(i, d[i]);
       }
@@ -331,7 +333,7 @@ layer_norm_bwd_kernel(int M, int D, int team, float eps, const T* __restrict__ r
     float sq = 0.f, sgc = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (i < live) {
+      if (i < kSure || i < live) {
         float gm[VEC];
         get_gamma(i, gm);
 #pragma unroll
@@ -347,7 +349,7 @@ layer_norm_bwd_kernel(int M, int D, int team, float eps, const T* __restrict__ r
     if (kAsync) asm volatile("cp.async.wait_group 2;" ::: "memory");  // dr too
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (i < live) {
+      if (i < kSure || i < live) {
         float gm[VEC], o[VEC];
         get_gamma(i, gm);
 #pragma unroll
@@ -377,7 +379,7 @@ layer_norm_bwd_kernel(int M, int D, int team, float eps, const T* __restrict__ r
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = c0 + i * gap;
-    if (i < live) {
+    if (i < kSure || i < live) {
 #pragma unroll
       for (int j = 0; j < VEC; ++j) { to[c + j] = ag[i][j]; to[D + c + j] = ab[i][j]; }
     }
@@ -511,8 +513,9 @@ cudaError_t bwd_t(const NormDims& d, const void* r, const float* gamma, const vo
     constexpr int kNv = decltype(nv)::value;
     constexpr bool kWide = decltype(wide)::value;
     auto kernel = layer_norm_bwd_kernel<T, G, VEC, kNv, kWide, kAsync, false>;
-    if constexpr (VEC > 1 && kNv * VEC == 16 && !kAsync && !kWide) {
-      if (gamma && sh.nv * VEC * sh.team == d.D) kernel = layer_norm_bwd_kernel<T, G, VEC, kNv, kWide, kAsync, true>;
+    if constexpr (!kWide && !kAsync && kNv * VEC == (VEC == 1 ? 8 : 16)) {
+      const int sure = VEC == 1 ? kNv - 1 : kNv;
+      if (gamma && sure * VEC * sh.team <= d.D) kernel = layer_norm_bwd_kernel<T, G, VEC, kNv, kWide, kAsync, true>;
     }
     const size_t rows = kAsync ? (size_t)sh.groups * sh.nv * sh.team * VEC * (sizeof(T) + 2 * sizeof(G)) : 0;
     const size_t sums = sh.groups > 1 ? (size_t)sh.groups * 2 * d.D * 4 : 0, smem = rows > sums ? rows : sums;

@@ -171,7 +171,7 @@ def norm_bwd_bounds(r, gamma, dy, dr, eps):
 
 
 @pytest.mark.parametrize("dt,gt", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16"), ("f16", "f32")])
-@pytest.mark.parametrize("M,D", NORM_SHAPES + [(2500, 96), (700, 768), (640, 760)])
+@pytest.mark.parametrize("M,D", NORM_SHAPES + [(2500, 96), (700, 768), (640, 760), (300, 223)])
 def test_layer_norm_bwd(M, D, dt, gt):
     code, t = TYPES[dt]
     gcode, gty = TYPES[gt]
