@@ -24,10 +24,11 @@ namespace {
 // as many teams as its threads allow.  Sums over a warp and addresses cost the same for few columns a thread as for many;
 // more threads hide more latency.  Columns of a thread, at most (M x D, dtype / gradients' dtype, measured):
 //   forward            16   32768 x 2048 bf16 with the residual sum: 88 us; 24 columns 102 us
+//     of odd widths     8   20000 x 1001 bf16 with the residual sum: 62 us; 16 columns (spills) 94 us
 //   16-bit gradients   16   8192 x 768 bf16 / f32 (12 columns): 25 us; 8 columns 32 us.  20000 x 2048 bf16 (16 columns,
 //                           one block of 384 threads an SM, whose registers do not spill): 94 us; two of 256 96 us
 //   f32 gradients       8   5000 x 1500: 35 us with the rows ahead in shared memory; 16 in registers 45 us
-//   odd widths          8   4099 x 1001 f32: 18 us with two blocks an SM; 4 columns 22 us, 8 with three (spills) 38 us
+//     of odd widths     8   4099 x 1001 f32: 18 us with two blocks an SM; 4 columns 22 us, 8 with three (spills) 38 us
 // 8 where there are few rows, and 16, 24 or, in blocks of 512 threads, 32 where a block would not hold the row otherwise.
 constexpr int kMaxThreads = 512;
 constexpr int threads_of(bool wide) { return wide ? kMaxThreads : 256; }
@@ -493,7 +494,7 @@ Shape bwd_shape(const NormDims& d) {
 template <class T, int VEC>
 cudaError_t fwd_t(const NormDims& d, const void* x, const void* residual, const float* gamma, const float* beta, void* y,
                   void* r_out, cudaStream_t s) {
-  const Shape sh = shape_of(d.M, d.D, VEC, 16, false, false);
+  const Shape sh = shape_of(d.M, d.D, VEC, VEC == 1 ? 8 : 16, false, false);
   with_shape<VEC>(sh, [&](auto nv, auto wide) {
     layer_norm_kernel<T, VEC, decltype(nv)::value, decltype(wide)::value><<<sh.blocks, sh.groups * sh.team, 0, s>>>(
         d.M, d.D, sh.team, d.x_stride, d.eps, (const T*)x, (const T*)residual, gamma, beta, (T*)y, (T*)r_out);
