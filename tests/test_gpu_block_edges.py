@@ -1,0 +1,75 @@
+"""The operators around the token mixer where values are small, far from zero or not finite, over many rows, and beside
+the layer itself: on the GPU through the C ABI, against 64-bit results, with bounds derived in each test.
+
+u = 2^-24 is fp32's rounding; a tensor stored in type t is rounded once, by at most finfo(t).eps / 2 of its value.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from parameter_space_moe_b200 import swimba
+from tests.test_gpu_block import TYPES, U, Out, ok, within
+
+pytestmark = pytest.mark.gpu
+
+_erfc = np.vectorize(math.erfc, otypes=[np.float64])
+
+
+# ------------------------------------------------------------------------------------------------ feed-forward
+def gelu_tail(g, dt):
+    """gelu(g) and its slope without cancellation, and the relative error of the kernel's tail, which its complement for
+    positive g keeps in absolute terms (at most as large relative to it, and one rounding)."""
+    z = -g / math.sqrt(2.0)
+    c = 0.5 * _erfc(z)
+    n = np.exp(-0.5 * g * g) / math.sqrt(2.0 * math.pi)
+    if dt != "f32":
+        # the exponent g^2 / 2 and its change of base carry four roundings; ex2, the quotient 2 ulp; the fit 2^-19.9;
+        # two products
+        return g * c, c + g * n, c, n, U * (4 * 0.5 * g * g + 4 + 4 + 2) + 2.0 ** -19.9
+    # z carries two roundings (the constant's and the product's), which erfc passes on by |z erfc'(z) / erfc(z)|;
+    # erfc itself is good to 4 ulp, 8 u
+    rel = U * (2 * np.abs(z) * 2 * np.exp(-z * z) / (math.sqrt(math.pi) * _erfc(z)) + 8)
+    return g * c, c + g * n, c, n, rel
+
+
+@pytest.mark.parametrize("dt", TYPES)
+def test_gelu_keeps_its_negative_tail(dt):
+    """h = gelu(g) up and its two factors' gradients for g in [-8, 8], element by element and relative to the value: the
+    products around them are exact (one non-zero term of 1 each)."""
+    code, t = TYPES[dt]
+    D = F = 264
+    g = torch.linspace(-8, 8, 256).to(t)
+    gn = g.double().numpy()
+    value, slope, c, n, rel = gelu_tail(gn, dt)
+    # forward: x = (g, 1, 0 ..), gate = x and up = x[256] = 1 by weights of zeros and ones
+    x = torch.zeros(1, D, dtype=t)
+    x[0, :256], x[0, 256] = g, 1
+    wg, wu = torch.zeros(F, D, dtype=t), torch.zeros(F, D, dtype=t)
+    wg[range(256), range(256)], wu[:, 256] = 1, 1
+    d = swimba.ffn_dims(1, D, F, code, swimba.GELU)
+    ws = torch.empty(max(swimba.gated_ffn_workspace_size(d), swimba.gated_ffn_bwd_workspace_size(d)), dtype=torch.uint8,
+                     device="cuda")
+    gate, up, h, out = (Out((1, k), t) for k in (F, F, F, D))
+    swimba.gated_ffn(d, x.cuda(), wg.cuda(), wu.cuda(), torch.zeros(D, F, dtype=t).cuda(), gate.t, up.t, h.t, out.t, ws)
+    ok()
+    assert np.array_equal(gate.np()[0, :256], gn) and (up.np() == 1).all()
+    # the cumulative term's error, then its half, times g, times up
+    within(h.np()[0, :256], value, np.abs(value) * (rel + 3 * U), t, f"gelu {dt}")
+    # backward: dh = 1, up = 1, x = (1, 0 ..), so that the first columns of dw_gate and dw_up are dgate and dup, rounded once
+    one = torch.zeros(1, D, dtype=t)
+    one[0, 0] = 1
+    wd = torch.zeros(D, F, dtype=t)
+    wd[0] = 1
+    stored = torch.zeros(1, F, dtype=t)
+    stored[0, :256] = g
+    dx, dwg, dwu, dwd = Out((1, D), t), Out((F, D), t), Out((F, D), t), Out((D, F), t)
+    swimba.gated_ffn_bwd(d, one.cuda(), stored.cuda(), torch.ones(1, F, dtype=t).cuda(), h.t, wg.cuda(), wu.cuda(), wd.cuda(),
+                         one.cuda(), dx.t, dwg.t, dwu.t, dwd.t, ws)
+    ok()
+    within(dwu.np()[:256, 0], value, np.abs(value) * (rel + 3 * U), t, "dup")
+    # the density: the exponent -g^2 / 2 and its change of base carry four roundings, ex2 2 ulp, the constant and two
+    # products one rounding each; then the sum's
+    e = c * rel + np.abs(gn) * n * U * (4 * 0.5 * gn * gn + 4 + 4) + U * np.abs(slope)
+    within(dwg.np()[:256, 0], slope, e + 2 * U * np.abs(slope), t, "dgate")
