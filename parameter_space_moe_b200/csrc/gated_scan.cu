@@ -29,7 +29,9 @@ namespace swimba {
 namespace {
 
 constexpr int kWarps = 4, kStages = 2;
-// CTAs whose registers fit an SM, by the tokens of a warp's round: the long rounds take twice as many.
+// CTAs whose registers fit an SM, by the tokens of a warp's round: the long rounds take twice as many.  The ways below cap
+// them by shared memory: three where 16-bit inputs meet fp32 gradients in short rounds, 61 KB a CTA (planned as four, a
+// launch of 512 CTAs took two turns: 1 x 2048 x 4096 44 us, 32 us so).
 constexpr int fwd_resident(int S, int lane_bytes) { return S * lane_bytes > 64 ? 2 : 4; }
 constexpr int bwd_resident(int S, int lane_bytes) { return S * lane_bytes > 32 ? 2 : 4; }
 
@@ -521,8 +523,12 @@ Split best_split(int groups, int rounds, int resident, double fixed, double each
   return best;
 }
 // Dynamic shared memory of which `per_sm` CTAs, and no more, fit an SM's 228 KB (1 KB of each CTA is the system's).
+constexpr size_t kSmSmem = 233472;
+constexpr int fitting(int ctas, size_t smem) {
+  return ctas * (smem + 1024) <= kSmSmem ? ctas : (int)(kSmSmem / (smem + 1024));
+}
 size_t smem_for(int per_sm, size_t need) {
-  const size_t share = (233472 / (size_t)per_sm - 1024) / 128 * 128;
+  const size_t share = (kSmSmem / (size_t)per_sm - 1024) / 128 * 128;
   return share > need ? share : need;
 }
 
@@ -571,8 +577,10 @@ auto fwd_way() {
   static std::atomic<unsigned long long> wide{0};
   auto kernel = gated_scan_kernel<T, V, S, kAsync>;
   using R = Rows<T, V, S, kAsync>;
-  return Way<decltype(kernel)>{kernel, 32 * V, kWarps * S, fwd_resident(S, V * sizeof(T)), kFixed, kEach,
-                               sizeof(Maps<V>) + (kAsync ? (size_t)kStages * kWarps * 2 * R::kBytes : 0), wide};
+  constexpr size_t kSmem = sizeof(Maps<V>) + (kAsync ? (size_t)kStages * kWarps * 2 * R::kBytes : 0);
+  constexpr int kResident = fitting(fwd_resident(S, V * sizeof(T)), kSmem);
+  static_assert(kResident * (kSmem + 1024) <= kSmSmem, "the planned CTAs fit an SM's shared memory");
+  return Way<decltype(kernel)>{kernel, 32 * V, kWarps * S, kResident, kFixed, kEach, kSmem, wide};
 }
 template <class T, class G, int V, int S, bool kAsync>
 auto bwd_way() {
@@ -582,8 +590,10 @@ auto bwd_way() {
   static std::atomic<unsigned long long> wide{0};
   auto kernel = gated_scan_bwd_kernel<T, G, V, S, kAsync>;
   constexpr size_t kWarpBytes = 3 * Rows<T, V, S, kAsync>::kBytes + Rows<G, V, S, kAsync>::kBytes;
-  return Way<decltype(kernel)>{kernel, 32 * V, kWarps * S, bwd_resident(S, V * sizeof(T)), kFixed, kEach,
-                               sizeof(Maps<V>) + (kAsync ? kStages * kWarps * kWarpBytes : 0), wide};
+  constexpr size_t kSmem = sizeof(Maps<V>) + (kAsync ? kStages * kWarps * kWarpBytes : 0);
+  constexpr int kResident = fitting(bwd_resident(S, V * sizeof(T)), kSmem);
+  static_assert(kResident * (kSmem + 1024) <= kSmSmem, "the planned CTAs fit an SM's shared memory");
+  return Way<decltype(kernel)>{kernel, 32 * V, kWarps * S, kResident, kFixed, kEach, kSmem, wide};
 }
 template <class K, class... A>
 cudaError_t launch(const Way<K>& w, const GatedDims& d, cudaStream_t s, A... a) {
