@@ -20,8 +20,8 @@
 // (gate and up at K = 768: 46 us, pipe 56 %; dgate and dup with their two more inputs: 159 us, 63 %), and
 // turns that do not fill the SMs (8192 x 768 from K = 2048: 96 tiles on 74 pairs, 30.7 us, 41 %).  256 rows: the weights'
 // bytes and each launch's start and end (256 x 2048 x 5632, 74 MB: 21 + 14 + 5 us alone, 32 us together).
-// Persistent over the units (problem, tile, split of K); a product with few tiles is split along K into fp32
-// partial sums, added in a fixed order by a second kernel.
+// Persistent over the units (problem, tile, split of K); a product with few tiles or a very long K is split along K into
+// fp32 partial sums, added in a fixed order by a second kernel.
 #include <math.h>
 
 #include "ffn_act.cuh"
@@ -42,7 +42,12 @@ constexpr uint32_t kStageBytes = 4 * kBox;          // two boxes of A, two of B
 constexpr uint32_t kBlock = 32 * 64;                // an epilogue warp's staged block: 32 rows of 64 bytes
 constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + kEpiWarps * kBlocks * kBlock + 256;
 constexpr int kSms = 148;                           // what the plan fills; the launch asks the device
-constexpr int kMaxSplit = 16;
+constexpr int kMaxSplit = 16;                       // of a product with few tiles
+// K blocks of one accumulation of 16-bit operands, at most.  The tensor cores cut what an addition shifts out: 1.1e-7 of
+// the sum for every 16 of K when all terms have one sign.  Over 2^20 rows in one chain the weights' gradients came out
+// 6.5e-3 small; 65536 of K leave 4.3e-4, a ninth of bf16's half step, 16384 1.1e-4, a quarter of fp16's
+// (the gradients at 32768 x 768 x 2048 fp16: 605 us in one chain, 636 us in two).
+constexpr int longest(int dtype) { return dtype == SWIMBA_BF16 ? 512 : 128; }
 
 struct Prob {
   int M, N, kbs, nkb, a_mn, b_mn;  // kbs: K blocks of a segment, nkb: of all
@@ -504,6 +509,8 @@ Plan make_plan(const FfnLaunch& l, Args* a) {
     const int kbs = ceil_div(q.K, BK), nkb = kbs * q.nseg;
     long long split = l.epi == kFfnStore && total < slots ? nkb / length : 1;
     split = split < 1 ? 1 : split > kMaxSplit ? kMaxSplit : split;
+    if (l.epi == kFfnStore && l.dtype != SWIMBA_F32 && split < ceil_div(nkb, longest(l.dtype)))
+      split = ceil_div(nkb, longest(l.dtype));
     if (a) {
       Prob& r = a->prob[p];
       r.M = q.M; r.N = q.N; r.kbs = kbs; r.nkb = nkb; r.a_mn = q.a_mn; r.b_mn = q.b_mn;

@@ -73,3 +73,37 @@ def test_gelu_keeps_its_negative_tail(dt):
     # products one rounding each; then the sum's
     e = c * rel + np.abs(gn) * n * U * (4 * 0.5 * gn * gn + 4 + 4) + U * np.abs(slope)
     within(dwg.np()[:256, 0], slope, e + 2 * U * np.abs(slope), t, "dgate")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("M,D,F", [(1 << 20, 64, 72), ((1 << 18) + 40, 264, 136)])
+def test_gradients_of_the_weights_over_many_rows(M, D, F, dt):
+    """Sums over a million rows of one sign: the tensor cores cut, they do not round, so an unbroken chain drifts."""
+    code, t = TYPES[dt]
+    gen = torch.Generator(device="cuda").manual_seed(M + D)
+    draw = lambda *s: (torch.rand(*s, generator=gen, device="cuda") + 0.5).to(t)
+    x, gate, up, h, dout = draw(M, D), draw(M, F), draw(M, F), draw(M, F), (draw(M, D) * 2.0 ** -10).to(t)
+    wd = draw(D, F) / 64
+    d = swimba.ffn_dims(M, D, F, code)
+    ws = torch.empty(swimba.gated_ffn_bwd_workspace_size(d), dtype=torch.uint8, device="cuda")
+    w = draw(F, D) / 64
+    dx, dwg, dwu, dwd = torch.empty_like(x), Out((F, D), t), Out((F, D), t), Out((D, F), t)
+    swimba.gated_ffn_bwd(d, x, gate, up, h, w, w, wd, dout, dx, dwg.t, dwu.t, dwd.t, ws)
+    ok()
+    want_d, want_u = torch.zeros(D, F, dtype=torch.float64, device="cuda"), torch.zeros(F, D, dtype=torch.float64, device="cuda")
+    rough = torch.zeros_like(want_u)
+    for i in range(0, M, 1 << 16):
+        j = slice(i, min(M, i + (1 << 16)))
+        want_d += dout[j].double().T @ h[j].double()
+        g = gate[j].double()
+        dup = (dout[j].double() @ wd.double()) * g * torch.sigmoid(g)
+        want_u += dup.T @ x[j].double()
+        rough += dup.abs().T @ x[j].double().abs()
+    # every term is positive, so a chain's running sum never passes its end: a step of 16 cuts less than 2^-23 of it, and
+    # a chain is 65536 of K (bf16) or 16384 (fp16) long; the split sums, 64 at most, add a rounding each
+    cut = (4096 if dt == "bf16" else 1024) * 2.0 ** -23 + 64 * U
+    want = want_d.cpu().numpy()
+    within(dwd.np(), want, cut * np.abs(want), t, f"dw_down {M}x{D}x{F} {dt}")
+    # dup is rounded to the type on its way, and its own product cuts K / 16 steps
+    want, rough = want_u.cpu().numpy(), rough.cpu().numpy()
+    within(dwu.np(), want, cut * np.abs(want) + (torch.finfo(t).eps / 2 + (D / 16 + 32) * 2.0 ** -23) * rough, t, "dw_up")
