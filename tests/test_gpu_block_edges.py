@@ -10,11 +10,105 @@ import pytest
 import torch
 
 from parameter_space_moe_b200 import swimba
-from tests.test_gpu_block import TYPES, U, Out, ok, within
+from tests.test_gpu_block import ROW_ADDS, TYPES, U, Out, ok, within
 
 pytestmark = pytest.mark.gpu
 
 _erfc = np.vectorize(math.erfc, otypes=[np.float64])
+
+
+# ------------------------------------------------------------------------------------------------ layer norm
+# Every layout of a row (columns a thread, one or several warps, single columns or vectors) over at least four rows a
+# team and a last turn that some teams sit out: the loads a row ahead, the steps of the pointers, the sums' two copies, the
+# room of the asynchronous copies.  The last entry is the layout of few rows, two a team.
+MANY_ROWS = [(14401, 29), (14401, 61), (14401, 93), (14401, 125), (14401, 189), (14401, 221), (14401, 253), (1801, 219),
+             (1801, 411), (1801, 659), (1801, 823), (1801, 1319), (1801, 1567), (1801, 2047), (1801, 2049), (1801, 5001),
+             (601, 8191), (601, 16383), (19001, 96), (19001, 132), (19001, 256), (14401, 264), (14401, 260), (14401, 384),
+             (14401, 500), (14401, 512), (7201, 768), (7201, 776), (2401, 876), (7201, 1000), (3601, 2048), (1801, 2052),
+             (1801, 2636), (1801, 3000), (1801, 4096), (1801, 4100), (1801, 4104), (1801, 5000), (601, 6148), (601, 6152),
+             (601, 8200), (601, 16384), (591, 1024)]
+
+
+def drawn(gen, shape, t, scale=1.0, shift=0.0):
+    return (torch.randn(shape, generator=gen, device="cuda") * scale + shift).to(t)
+
+
+def near(got, ref, bound, t, what):
+    """within() on the GPU: |got - ref| <= bound + the one rounding to t."""
+    eps, low = torch.finfo(t).eps / 2, torch.finfo(t).smallest_normal * torch.finfo(t).eps / 2
+    tol = 1.01 * (bound + eps * (ref.abs() + bound)) + low
+    worst = ((got.double() - ref).abs() / tol).max()
+    assert bool(torch.isfinite(got).all()) and float(worst) <= 1.0, f"{what}: {float(worst):.3f} of its bound"
+
+
+def row_stats(r, eps):
+    """xhat, rstd, and the errors of xhat and (relative) of rstd in fp32: the row's mean is off by ROW_ADDS u mean|r|, a
+    centred value by that, its own rounding and the difference's; the variance by twice that over its terms and its sum."""
+    mu = r.mean(1, keepdim=True)
+    rstd = 1 / torch.sqrt(((r - mu) ** 2).mean(1, keepdim=True) + eps)
+    xhat = (r - mu) * rstd
+    dev = U * (ROW_ADDS * r.abs().mean(1, keepdim=True) + r.abs()) * rstd + U * xhat.abs()
+    rel = (dev * xhat.abs()).mean(1, keepdim=True) + U * (ROW_ADDS + 8)
+    return xhat, rstd, dev + rel * xhat.abs(), rel
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("M,D", MANY_ROWS)
+def test_layer_norm_over_many_rows(M, D, dt):
+    """Rows of a wider tensor, the residual stream updated in place."""
+    code, t = TYPES[dt]
+    eps = float(np.float32(1e-5))
+    gen = torch.Generator(device="cuda").manual_seed(M + D)
+    x, res = drawn(gen, (M, D + 8), t, 1.5, 0.7)[:, :D], Out((M, D), t)
+    res.t.copy_(drawn(gen, (M, D), t, 3.0, -0.4))
+    gamma, beta = drawn(gen, (D,), torch.float32, 0.3, 1.0), drawn(gen, (D,), torch.float32, 0.3)
+    r = x.double() + res.t.double()
+    y = Out((M, D), t)
+    swimba.layer_norm(swimba.norm_dims(M, D, code, x_stride=D + 8, eps=eps), x, res.t, gamma, beta, y.t, res.t)
+    ok()
+    xhat, _, dx, _ = row_stats(r, eps)
+    near(y.t, xhat * gamma.double() + beta.double(), dx * gamma.double().abs()
+         + 3 * U * (xhat.abs() * gamma.double().abs() + beta.double().abs()), t, f"y {M}x{D} {dt}")
+    near(res.t, r, U * r.abs(), t, "r")
+    y.np(), res.np()  # nothing is written behind them
+
+
+@pytest.mark.parametrize("dt,gt", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16"), ("f16", "f32")])
+@pytest.mark.parametrize("M,D", MANY_ROWS)
+def test_layer_norm_gradients_over_many_rows(M, D, dt, gt):
+    """With gamma and the gradient that reaches r past the norm (dx over it), and without either."""
+    (code, t), (gcode, g_t) = TYPES[dt], TYPES[gt]
+    eps = float(np.float32(1e-5))
+    gen = torch.Generator(device="cuda").manual_seed(M * 3 + D)
+    r, gamma = drawn(gen, (M, D), t, 2.0, 0.5), drawn(gen, (D,), torch.float32, 0.3, 1.0)
+    dy, dr = drawn(gen, (M, D), g_t, 0.5), drawn(gen, (M, D), g_t, 0.5)
+    d = swimba.norm_dims(M, D, code, gcode, eps=eps)
+    ws = torch.empty(swimba.layer_norm_bwd_workspace_size(d), dtype=torch.uint8, device="cuda")
+    mean = lambda v: v.mean(1, keepdim=True)
+    rd, dyd = r.double(), dy.double()
+    xhat, rstd, dxhat, rel = row_stats(rd, eps)
+    for gm, past in ((gamma, dr), (None, None)):
+        dx, dg, db = Out((M, D), g_t), Out((D,), torch.float32), Out((D,), torch.float32)
+        if past is not None:
+            dx.t.copy_(past)
+        swimba.layer_norm_bwd(d, r, gm, dy, dx.t if past is not None else None, dx.t, dg.t, db.t, ws)
+        ok()
+        ga = torch.ones(D, dtype=torch.float64, device="cuda") if gm is None else gm.double()
+        g = dyd * ga
+        want = rstd * (g - mean(g) - xhat * mean(g * xhat))
+        mg, mgx = mean(g.abs()), mean(g.abs() * xhat.abs())
+        inner = g.abs() + mg + xhat.abs() * mgx
+        bound = rstd * (U * (ROW_ADDS + 2) * mg + dxhat * mgx + xhat.abs() * (mean(g.abs() * dxhat) + U * (ROW_ADDS + 4) * mgx)
+                        + (4 * U + rel) * inner)
+        if past is not None:
+            want = want + past.double()
+            bound = bound + U * (past.double().abs() + rstd * inner)
+        near(dx.t, want, bound, g_t, f"dx {M}x{D} {dt}/{gt}")
+        # a column's sum: a team's rows, then the block's teams, at most 19 partial rows in a thread and 32 threads
+        adds = M / 148 + 1 + 16 + 19 + 32
+        near(dg.t, (dyd * xhat).sum(0), (dyd.abs() * (dxhat + (adds + 1) * U * xhat.abs())).sum(0), torch.float32, "dgamma")
+        near(db.t, dyd.sum(0), adds * U * dyd.abs().sum(0), torch.float32, "dbeta")
+        dx.np(), dg.np(), db.np()
 
 
 # ------------------------------------------------------------------------------------------------ feed-forward
