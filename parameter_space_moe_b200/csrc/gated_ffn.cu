@@ -20,8 +20,9 @@ namespace swimba {
 namespace {
 
 // Operands of the block's launches are 16-bit tensors as they are, or an fp32 tensor's three bf16 planes; a product of two
-// fp32 tensors is then the six products of planes i and j with i + j <= 2, as six segments of K (the terms left out are
-// below 2^-26 of it).  On CUDA cores the same products took five to seven times as long from 16 x 512 x 1024 on.
+// fp32 tensors is then the six products of planes i and j with i + j <= 2, as six segments of K.  The planes are below
+// 2^-8 and 2^-17 of the value, so a pair left out is below 2^-25 of the product and all three together below 2^-24.  On
+// CUDA cores the same products took five to seven times as long from 16 x 512 x 1024 on.
 void add_segments(FfnProblem& q, int a, int b, int b_up, int planes) {
   for (int i = planes - 1; i >= 0; --i)  // the small terms first
     for (int j = planes - 1 - i; j >= 0; --j) {

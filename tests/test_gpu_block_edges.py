@@ -9,8 +9,12 @@ import numpy as np
 import pytest
 import torch
 
-from parameter_space_moe_b200 import swimba
-from tests.test_gpu_block import ROW_ADDS, TYPES, U, Out, ok, within
+from oracle import block_oracle as O
+from oracle import swimba_oracle as S
+from parameter_space_moe_b200 import configs, inputs, swimba
+
+from .parity import check_topk, device_weights, f64, out_dtype, tol_of
+from .test_gpu_block import ROW_ADDS, TYPES, U, Out, ok, within
 
 pytestmark = pytest.mark.gpu
 
@@ -201,3 +205,55 @@ def test_gradients_of_the_weights_over_many_rows(M, D, F, dt):
     # dup is rounded to the type on its way, and its own product cuts K / 16 steps
     want, rough = want_u.cpu().numpy(), rough.cpu().numpy()
     within(dwu.np(), want, cut * np.abs(want) + (torch.finfo(t).eps / 2 + (D / 16 + 32) * 2.0 ** -23) * rough, t, "dw_up")
+
+
+def chained(K, planes=6):
+    """Norm-wise error of an fp32 product over K on three bf16 planes a tensor, random signs.  A chain is 256 of K: 16
+    steps that each cut less than 2^-23 of the running sum, which is at most the chain's end; the chains' cuts have their
+    chains' signs and add up like them.  The chains, 6 K / 256 of them, are added with a rounding of u each, independent
+    ones; the plane products left out are 2^-24 of the whole, the result is rounded once."""
+    return 16 * 2.0 ** -23 + U * (math.sqrt(planes * K / 256 + planes) + 2)
+
+
+def normwise(got, ref, bar, what):
+    e = float((got.double() - ref).norm() / ref.norm())
+    print(f"{what}: {e:.2e} of {bar:.2e}")
+    assert e <= bar, what
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+@pytest.mark.parametrize("M,D,F", [(300, 768, 2816), (2900, 264, 1032), (130, 2816, 264), (5000, 520, 3000)])
+def test_fp32_products_keep_their_accuracy(M, D, F, kind):
+    """Norm-wise, each product from the operands that the GPU holds: an unbroken chain (2e-5 at 12 x 2816) or a plane
+    product left out (2^-16) is many times the bar."""
+    gen = torch.Generator(device="cuda").manual_seed(M + F)
+    draw = lambda *s, std=1.0: drawn(gen, s, torch.float32, std)
+    x, dout = draw(M, D), draw(M, D)
+    wg, wu, wd = draw(F, D, std=D ** -0.5), draw(F, D, std=D ** -0.5), draw(D, F, std=F ** -0.5)
+    d = swimba.ffn_dims(M, D, F, swimba.F32, swimba.SILU if kind == "silu" else swimba.GELU)
+    ws = torch.empty(max(swimba.gated_ffn_workspace_size(d), swimba.gated_ffn_bwd_workspace_size(d)), dtype=torch.uint8,
+                     device="cuda")
+    gate, up, h, out = (torch.empty(M, k, device="cuda") for k in (F, F, F, D))
+    swimba.gated_ffn(d, x, wg, wu, wd, gate, up, h, out, ws)
+    dx, dwg, dwu, dwd = torch.empty_like(x), torch.empty_like(wg), torch.empty_like(wu), torch.empty_like(wd)
+    swimba.gated_ffn_bwd(d, x, gate, up, h, wg, wu, wd, dout, dx, dwg, dwu, dwd, ws)
+    ok()
+    x, dout, wg, wu, wd, G, P, H = (v.double() for v in (x, dout, wg, wu, wd, gate, up, h))
+    normwise(gate, x @ wg.T, chained(D), "gate")
+    normwise(up, x @ wu.T, chained(D), "up")
+    if kind == "silu":
+        s = torch.sigmoid(G)
+        act, slope = G * s, s * (1 + G * (1 - s))
+    else:
+        c = 0.5 * torch.special.erfc(-G / math.sqrt(2.0))
+        act, slope = G * c, c + G * torch.exp(-0.5 * G * G) / math.sqrt(2 * math.pi)
+    # h is formed from the sums that gate and up are stored from: the same values in fp32
+    normwise(h, act * P, 16 * U, "h")
+    normwise(out, H @ wd.T, chained(F), "out")
+    dh = dout @ wd
+    dg, du = dh * P * slope, dh * act
+    # the products behind dgate and dup carry dh's error and the activation's 32 u, which random signs pass on as they are
+    normwise(dx, dg @ wg + du @ wu, chained(2 * F) + chained(D) + 32 * U, "dx")
+    normwise(dwg, dg.T @ x, chained(M) + chained(D) + 32 * U, "dw_gate")
+    normwise(dwu, du.T @ x, chained(M) + chained(D) + 32 * U, "dw_up")
+    normwise(dwd, dout.T @ H, chained(M), "dw_down")
