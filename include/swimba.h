@@ -329,7 +329,9 @@ typedef struct {
  *   f_t = sigmoid(gate_t),  h_t = f_t h_{t-1} + (1 - f_t) x_t,  h_{-1} = init_state or 0
  *   x, gate [B][T][W], tokens x_stride and gate_stride apart; init_state [B][W] fp32 or NULL
  *   h [B][T][W] dtype out; final_state [B][W] fp32 out or NULL (may be init_state)
- * Where x is not finite, h is not finite from that token until the state is forgotten. */
+ * Where x or the state is not finite, that channel's h is not finite from that token on (a closed gate multiplies the
+ * state by 0, which gives NaN).  A device status of SWIMBA_ERR_TIMEOUT, here and from the gradients, means a bounded
+ * wait between the CTAs of a cluster gave up (outputs invalid). */
 swimba_status swimba_gated_scan(const swimba_gated_dims* dims, const void* x, const void* gate, const float* init_state,
                                 void* h, float* final_state, void* stream);
 

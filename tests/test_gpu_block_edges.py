@@ -115,6 +115,30 @@ def test_layer_norm_gradients_over_many_rows(M, D, dt, gt):
         dx.np(), dg.np(), db.np()
 
 
+# ------------------------------------------------------------------------------------------------ gated scan
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("T,W", [(400, 64), (2100, 33)])
+def test_what_is_not_finite_stays_in_its_channel_for_good(T, W, dt):
+    """A state that is not finite stays so: f = 0 times it is NaN.  The other channels keep their bits."""
+    code, t = TYPES[dt]
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    x, gate = drawn(gen, (1, T, W), t), drawn(gen, (1, T, W), t)
+    gate[:, 250] = -float("inf")
+    want, h = torch.empty_like(x), torch.empty_like(x)
+    fin = torch.empty(1, W, device="cuda")
+    d = swimba.gated_dims(1, T, W, code)
+    swimba.gated_scan(d, x, gate, None, want, None)
+    x[0, 41, 7], x[0, 137, 20] = float("inf"), float("nan")
+    swimba.gated_scan(d, x, gate, None, h, fin)
+    ok()
+    assert torch.equal(want[0, 250], x[0, 250])
+    for c, first in ((7, 41), (20, 137)):
+        assert not bool(torch.isfinite(h[0, first:, c]).any()) and not bool(torch.isfinite(fin[0, c]))
+        assert torch.equal(h[0, :first, c], want[0, :first, c])
+    rest = [c for c in range(W) if c not in (7, 20)]
+    assert torch.equal(h[..., rest], want[..., rest]) and bool(torch.isfinite(fin[0, rest]).all())
+
+
 # ------------------------------------------------------------------------------------------------ feed-forward
 def gelu_tail(g, dt):
     """gelu(g) and its slope without cancellation, and the relative error of the kernel's tail, which its complement for
