@@ -368,9 +368,10 @@ size_t swimba_gated_ffn_bwd_workspace_size(const swimba_ffn_dims* dims);
  *   x [M][D]; w_gate, w_up [F][D]; w_down [D][F]
  *   gate, up [M][F] out, each or NULL (kept for the gradients); h [M][F] out; out [M][D] out
  * Products accumulate in fp32; h is formed from the fp32 values and rounded once, and the last product reads the
- * rounded h.  fp32 tensors are split into three bf16 tensors each, whose products keep fp32's accuracy; results that
- * depend on an infinite input are then NaN.  A device status of SWIMBA_ERR_TIMEOUT means a bounded wait of the
- * tensor-core kernel gave up (outputs invalid). */
+ * rounded h.  fp32 tensors are split into three bf16 tensors each, whose products keep fp32's accuracy down to values of
+ * 2^-108; smaller ones are off by up to 2^-134 (half of bf16's smallest subnormal).  Results that depend on an infinite
+ * fp32 input are not finite: infinite, or NaN where plane products of both signs meet or a plane is 0.  A device status
+ * of SWIMBA_ERR_TIMEOUT means a bounded wait of the tensor-core kernel gave up (outputs invalid). */
 swimba_status swimba_gated_ffn(const swimba_ffn_dims* dims, const void* x, const void* w_gate, const void* w_up,
                                const void* w_down, void* gate, void* up, void* h, void* out, void* ws, size_t ws_bytes,
                                void* stream);

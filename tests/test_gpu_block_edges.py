@@ -281,3 +281,46 @@ def test_fp32_products_keep_their_accuracy(M, D, F, kind):
     normwise(dwg, dg.T @ x, chained(M) + chained(D) + 32 * U, "dw_gate")
     normwise(dwu, du.T @ x, chained(M) + chained(D) + 32 * U, "dw_up")
     normwise(dwd, dout.T @ H, chained(M), "dw_down")
+
+
+@pytest.mark.parametrize("exponent", [-100, -114, -126])
+def test_fp32_small_values(exponent):
+    """A value's third plane ends at bf16's smallest subnormal, 2^-133: below 2^-108 it is off by up to half of that."""
+    M, D, F = 256, 64, 128
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    h, w, wd = drawn(gen, (M, F), torch.float32), drawn(gen, (F, D), torch.float32), drawn(gen, (D, F), torch.float32)
+    dout = torch.ldexp(drawn(gen, (M, D), torch.float32), torch.tensor(float(exponent), device="cuda"))
+    d = swimba.ffn_dims(M, D, F, swimba.F32)
+    ws = torch.empty(swimba.gated_ffn_bwd_workspace_size(d), dtype=torch.uint8, device="cuda")
+    dx, dwg, dwu, dwd = torch.empty(M, D, device="cuda"), torch.empty_like(w), torch.empty_like(w), torch.empty_like(wd)
+    swimba.gated_ffn_bwd(d, torch.ones(M, D, device="cuda"), h, h, h, w, w, wd, dout, dx, dwg, dwu, dwd, ws)
+    ok()
+    want, size = dout.double().T @ h.double(), dout.double().abs().T @ h.double().abs()
+    # one chain of 256 a plane product; the results are stored down to fp32's own subnormals
+    tol = (16 * 2.0 ** -23 + 8 * U) * size + 2.0 ** -134 * h.double().abs().sum(0) + 2.0 ** -149
+    assert bool(((dwd.double() - want).abs() <= tol).all())
+
+
+def test_fp32_infinities_stay_in_their_rows():
+    """An infinite input makes what depends on it not finite (infinite, or NaN where plane products of both signs meet or a
+    plane is 0) and leaves the other rows their bits."""
+    M, D, F = 140, 72, 136
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    x = drawn(gen, (M, D), torch.float32)
+    wg, wu, wd = drawn(gen, (F, D), torch.float32), drawn(gen, (F, D), torch.float32), drawn(gen, (D, F), torch.float32)
+    d = swimba.ffn_dims(M, D, F, swimba.F32)
+    ws = torch.empty(swimba.gated_ffn_workspace_size(d), dtype=torch.uint8, device="cuda")
+    outs = []
+    for bad in (False, True):
+        if bad:
+            x[3, 5], x[77, 70] = float("inf"), -float("inf")
+        gate, up, h, out = (torch.empty(M, k, device="cuda") for k in (F, F, F, D))
+        swimba.gated_ffn(d, x, wg, wu, wd, gate, up, h, out, ws)
+        ok()
+        outs.append((gate, up, h, out))
+    rest = [m for m in range(M) if m not in (3, 77)]
+    for a, b in zip(*outs):
+        assert bool(torch.isfinite(a).all()) and torch.equal(a[rest], b[rest])
+    for v in outs[1][:2]:
+        assert not bool(torch.isfinite(v[[3, 77]]).any())
+    assert bool(torch.isnan(outs[1][3][[3, 77]]).all())   # both signs, or NaN, among the hidden features
