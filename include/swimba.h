@@ -380,7 +380,9 @@ swimba_status swimba_gated_ffn(const swimba_ffn_dims* dims, const void* x, const
  *   dh = dout W_down,  dgate = dh up act'(gate),  dup = dh act(gate)
  *   dx [M][D] = dgate W_gate + dup W_up,  dw_gate [F][D] = dgate^T x,  dw_up [F][D] = dup^T x,
  *   dw_down [D][F] = dout^T h                                                  (all dtype, all out)
- * dgate and dup are formed from the fp32 dh and rounded once to dtype between the products. */
+ * dgate and dup are formed from the fp32 dh and rounded once to dtype between the products.  They are somewhat smaller
+ * than dout: in fp16 the caller scales the loss so that dout lies well above the subnormals (6e-5), whose digits the sums
+ * over all rows cannot bring back. */
 swimba_status swimba_gated_ffn_bwd(const swimba_ffn_dims* dims, const void* x, const void* gate, const void* up,
                                    const void* h, const void* w_gate, const void* w_up, const void* w_down,
                                    const void* dout, void* dx, void* dw_gate, void* dw_up, void* dw_down, void* ws,

@@ -324,3 +324,36 @@ def test_fp32_infinities_stay_in_their_rows():
     for v in outs[1][:2]:
         assert not bool(torch.isfinite(v[[3, 77]]).any())
     assert bool(torch.isnan(outs[1][3][[3, 77]]).all())   # both signs, or NaN, among the hidden features
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("exponent", [-14, -7, 5])
+def test_gradients_of_small_and_large_losses(exponent, dt):
+    """Upstream gradients from fp16's subnormals to 2^7: dgate and dup are rounded to the type, subnormal spacing
+    included, which is why the caller scales an fp16 loss."""
+    code, t = TYPES[dt]
+    M, D, F = 300, 264, 520
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x, gate, up, h = (drawn(gen, s, t) for s in ((M, D), (M, F), (M, F), (M, F)))
+    wg, wu, wd = (drawn(gen, s, t, s[1] ** -0.5) for s in ((F, D), (F, D), (D, F)))
+    dout = drawn(gen, (M, D), t, 2.0 ** exponent)
+    d = swimba.ffn_dims(M, D, F, code)
+    ws = torch.empty(swimba.gated_ffn_bwd_workspace_size(d), dtype=torch.uint8, device="cuda")
+    dx, dwg, dwu, dwd = Out((M, D), t), Out((F, D), t), Out((F, D), t), Out((D, F), t)
+    swimba.gated_ffn_bwd(d, x, gate, up, h, wg, wu, wd, dout, dx.t, dwg.t, dwu.t, dwd.t, ws)
+    ok()
+    x, dout, wg, wu, wd, g, u, h = (v.double() for v in (x, dout, wg, wu, wd, gate, up, h))
+    s = torch.sigmoid(g)
+    act, slope = g * s, s * (1 + g * (1 - s))
+    dot = lambda a, b: 2 * U * a.shape[1] * (a.abs() @ b.abs())
+    eps, low = torch.finfo(t).eps / 2, torch.finfo(t).smallest_normal * torch.finfo(t).eps / 2
+    dh, e = dout @ wd, dot(dout, wd)
+    dg, du = dh * u * slope, dh * act
+    bg = e * (u * slope).abs() + 32 * U * (dh * u).abs() * (1 + g.abs())
+    bu = e * act.abs() + 16 * U * (dh * g).abs()
+    rg, ru = (b + eps * (v.abs() + b) + low for v, b in ((dg, bg), (du, bu)))
+    near(dx.t, dg @ wg + du @ wu, 2 * (dot(dg, wg) + dot(du, wu)) + rg @ wg.abs() + ru @ wu.abs(), t, "dx")
+    near(dwg.t, dg.T @ x, dot(dg.T, x) + rg.T @ x.abs(), t, "dw_gate")
+    near(dwu.t, du.T @ x, dot(du.T, x) + ru.T @ x.abs(), t, "dw_up")
+    near(dwd.t, dout.T @ h, dot(dout.T, h), t, "dw_down")
+    dx.np(), dwg.np(), dwu.np(), dwd.np()
