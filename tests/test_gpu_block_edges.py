@@ -357,3 +357,93 @@ def test_gradients_of_small_and_large_losses(exponent, dt):
     near(dwu.t, du.T @ x, dot(du.T, x) + ru.T @ x.abs(), t, "dw_up")
     near(dwd.t, dout.T @ h, dot(dout.T, h), t, "dw_down")
     dx.np(), dwg.np(), dwu.np(), dwd.np()
+
+
+# ------------------------------------------------------------------------------------------------ beside the layer
+@pytest.mark.parametrize("w", [configs.TINY_F32.with_(name="row_f32", seqlen=200, seed=151),
+                               configs.BASE.with_(name="row_bf16", batch=2, seqlen=300, d_model=128, nheads=2, n_experts=4,
+                                                  chunk=128, seed=152)], ids=lambda w: w.name)
+def test_a_row_with_the_layer(w):
+    """Norm, the Swimba layer, output projection, norm over the residual sum, feed-forward block, then the gradients of
+    the block, the second norm, the layer (fp32, for a seeded dy) and the first norm (fp32 gradients beside its type), all
+    in a row on one stream without a pause.  Every call's result is held to its operator's 64-bit result on what the GPU
+    gave it; the row with a pause behind every call gives the same bits
+    up to the layer's gradients."""
+    B, T, D, F, M, HP = w.batch, w.seqlen, w.d_model, 256, w.M, w.nheads * w.headdim
+    t = out_dtype(w)
+    code = swimba.F32 if t is torch.float32 else swimba.BF16
+    inp = inputs.make_inputs(w)
+    d, W = swimba.dims_of(w), device_weights(inp)
+    gen = torch.Generator(device="cuda").manual_seed(w.seed)
+    f32 = torch.float32
+    x, dout, dy = drawn(gen, (M, D), t), drawn(gen, (M, D), t, 0.3), drawn(gen, (M, HP), f32)
+    g1, b1, g2, b2 = (drawn(gen, (D,), f32, 0.2, m) for m in (1.0, 0.0, 1.0, 0.0))
+    wg, wu, wd = (drawn(gen, s, t, s[1] ** -0.5) for s in ((F, D), (F, D), (D, F)))
+    w_out = inp["W_out"].cuda()
+    nd, n32, fd = swimba.norm_dims(M, D, code), swimba.norm_dims(M, D, code, swimba.F32), swimba.ffn_dims(M, D, F, code)
+    ws = torch.empty(max(swimba.layer_bwd_workspace_size(d), swimba.gated_ffn_workspace_size(fd),
+                         swimba.gated_ffn_bwd_workspace_size(fd), swimba.layer_norm_bwd_workspace_size(n32)),
+                     dtype=torch.uint8, device="cuda")
+
+    def row(pause):
+        new = lambda *s, ty=t: torch.full(s, float("nan"), dtype=ty, device="cuda")
+        v = dict(n1=new(M, D), y=new(M, HP), p=new(M, D), n2=new(M, D), r=new(M, D), gate=new(M, F), up=new(M, F),
+                 h=new(M, F), out=new(M, D), dn2=new(M, D), dr=new(M, D), dg2=new(D, ty=f32), db2=new(D, ty=f32),
+                 dn1=new(M, D, ty=f32), dx=new(M, D, ty=f32), dg1=new(D, ty=f32), db1=new(D, ty=f32))
+        idx = torch.empty(M, w.top_k, dtype=torch.int32, device="cuda")
+        lw = [new(*s, ty=f32) for s in ((w.n_experts, D), (w.nheads, D), (w.nheads,), (w.nheads,), (w.n_experts, w.W_e, D))]
+        dwg, dwu, dwd = new(F, D), new(F, D), new(D, F)
+        torch.cuda.synchronize()
+        for call in (lambda: swimba.layer_norm(nd, x, None, g1, b1, v["n1"], None),
+                     lambda: swimba.layer_fwd(d, v["n1"], W, None, v["y"], None, idx, None, ws),
+                     lambda: swimba.out_proj(d, v["y"], w_out, v["p"]),
+                     lambda: swimba.layer_norm(nd, v["p"], x, g2, b2, v["n2"], v["r"]),
+                     lambda: swimba.gated_ffn(fd, v["n2"], wg, wu, wd, v["gate"], v["up"], v["h"], v["out"], ws),
+                     lambda: swimba.gated_ffn_bwd(fd, v["n2"], v["gate"], v["up"], v["h"], wg, wu, wd, dout, v["dn2"], dwg, dwu,
+                                                  dwd, ws),
+                     lambda: swimba.layer_norm_bwd(nd, v["r"], g2, v["dn2"], dout, v["dr"], v["dg2"], v["db2"], ws),
+                     lambda: swimba.layer_bwd(d, v["n1"], W, None, dy, v["dn1"], *lw, None, ws),
+                     lambda: swimba.layer_norm_bwd(n32, x, g1, v["dn1"], None, v["dx"], v["dg1"], v["db1"], ws)):
+            call()
+            if pause:
+                torch.cuda.synchronize()
+        ok()
+        return v, idx
+
+    row(False)
+    (v, idx), (slow, _) = row(False), row(True)
+    for k in v:
+        assert bool(torch.isfinite(v[k]).all()), k
+        if k not in ("dn1", "dx", "dg1", "db1"):    # the layer's gradients are summed by atomics, in any order
+            assert torch.equal(v[k], slow[k]), k
+    n = {k: a.double().cpu().numpy() for k, a in v.items()}
+    num = lambda a: a.double().cpu().numpy()
+    eps = float(np.float32(1e-5))
+    own = 1e-5 if code == swimba.F32 else 2.0 ** -8    # one rounding, beside which the fp32 sums' are nothing
+    layer = tol_of(w)
+    held = lambda got, ref, bar, what: normwise(torch.from_numpy(got), torch.from_numpy(ref.reshape(got.shape)), bar, what)
+    held(n["n1"], O.layer_norm(num(x), None, num(g1), num(b1), eps)[0], own, "n1")
+    X = n["n1"].reshape(B, T, D)
+    weights = [f64(inp[k]) for k in ("W_r", "W_dt", "b_dt", "A", "W_exp")]
+    fl, forced = check_topk(idx.cpu().numpy(), S.router_logits(n["n1"], weights[0]), w.top_k)
+    forced = forced.reshape(B, T, w.top_k) if fl.any() else None
+    shape = (w.nheads, w.headdim, w.dstate, w.G, w.top_k)
+    held(n["y"], S.layer_fwd(X, *weights, *shape, forced_idx=forced)["y"], layer, "y")
+    held(n["p"], S.out_proj(n["y"], f64(inp["W_out"])), layer, "projection")
+    n2, r = O.layer_norm(n["p"], num(x), num(g2), num(b2), eps)
+    held(n["n2"], n2, own, "n2")
+    held(n["r"], r, own, "r")
+    gate, up, h, out = O.gated_ffn(n["n2"], num(wg), num(wu), num(wd), "silu")
+    for k, ref in (("gate", gate), ("up", up), ("h", h), ("out", out)):
+        held(n[k], ref, (2 if k == "out" else 1) * own, k)
+    dn2 = O.gated_ffn_bwd(n["n2"], n["gate"], n["up"], n["h"], num(wg), num(wu), num(wd), num(dout), "silu")[0]
+    held(n["dn2"], dn2, 2 * own, "dn2")
+    dr, dg2, db2 = O.layer_norm_bwd(n["r"], num(g2), n["dn2"], num(dout), eps)
+    held(n["dr"], dr, own, "dr")
+    held(n["dg2"], dg2, 1e-5, "dg2")
+    held(n["db2"], db2, 1e-5, "db2")
+    held(n["dn1"], S.layer_bwd(X, *weights, *shape, num(dy).reshape(B, T, w.nheads, w.headdim), None, forced)["dX"], layer,
+         "dn1")
+    dx, dg1, db1 = O.layer_norm_bwd(num(x), num(g1), n["dn1"], None, eps)
+    for k, ref in (("dx", dx), ("dg1", dg1), ("db1", db1)):
+        held(n[k], ref, 1e-5, k)
