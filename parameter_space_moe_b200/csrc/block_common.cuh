@@ -104,8 +104,9 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[VEC]) {
   }
 }
 
-// e^x and 1 / x by the hardware's approximations alone (2 ulp and 1 ulp; subnormal results and operands are 0), where
-// __expf and __fdividef add instructions for subnormals.
+// e^x and 1 / x by the hardware's approximations alone, where __expf and __fdividef add instructions for subnormals
+// (results and operands that are subnormal are 0 here).  The approximations are good to 2 ulp and 1 ulp; the product with
+// log2(e) rounds twice more, which adds 2 |x| u to e^x.
 __device__ __forceinline__ float exp_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));

@@ -53,7 +53,6 @@ struct Prob {
   int M, N, kbs, nkb, a_mn, b_mn;  // kbs: K blocks of a segment, nkb: of all
   unsigned char a[12], a_plane[12], b[12], b_plane[12], b_up[12];
   int tiles_m, tiles_n, split, begin;  // first unit
-  int out;      // number of its output's map
   void* dst;    // the output itself, and
   float* part;  // its partial sums [split][M][N] where split > 1
 };
@@ -69,7 +68,7 @@ struct Args {
 
 struct Maps {
   CUtensorMap m[kFfnMaxOperands];
-  CUtensorMap o[kFfnMaxProblems + 2];
+  CUtensorMap o[kFfnMaxProblems + 2];  // one per problem (its output, or its partial sums), then out2 and out3
 };
 
 struct Unit {
@@ -364,7 +363,7 @@ ffn_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
             if (a.out3 >= 0) store_block<T>(&maps.o[a.out3], staged, turn, lane, w, n, mw, 0);
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = act_value<kAct, sizeof(T) == 4>(v[i]) * w[i];
-            store_block<T>(&maps.o[q.out], staged, turn, lane, v, n, mw, 0);
+            store_block<T>(&maps.o[t.p], staged, turn, lane, v, n, mw, 0);
           }
         } else if (kEpi == kFfnDglu) {
           if (!kAhead) fetch(c);
@@ -378,12 +377,12 @@ ffn_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
               w[i] = v[i] * act;
               v[i] *= cu.get(i) * slope;
             }
-            store_block<T>(&maps.o[q.out], staged, turn, lane, v, n, mw, 0);
+            store_block<T>(&maps.o[t.p], staged, turn, lane, v, n, mw, 0);
             store_block<T>(&maps.o[a.out2], staged, turn, lane, w, n, mw, 0);
           }
         } else if (some) {
-          if (q.split > 1) store_block<float>(&maps.o[q.out], staged, turn, lane, v, n, mw, t.s);
-          else store_block<T>(&maps.o[q.out], staged, turn, lane, v, n, mw, 0);
+          if (q.split > 1) store_block<float>(&maps.o[t.p], staged, turn, lane, v, n, mw, t.s);
+          else store_block<T>(&maps.o[t.p], staged, turn, lane, v, n, mw, 0);
         }
       };
       bool ok = true;
@@ -516,7 +515,6 @@ Plan make_plan(const FfnLaunch& l, Args* a) {
       r.M = q.M; r.N = q.N; r.kbs = kbs; r.nkb = nkb; r.a_mn = q.a_mn; r.b_mn = q.b_mn;
       for (int s = 0; s < 12; ++s) { r.a[s] = q.a[s]; r.b[s] = q.b[s]; r.a_plane[s] = q.a_plane[s]; r.b_plane[s] = q.b_plane[s]; r.b_up[s] = q.b_up[s]; }
       r.tiles_m = ceil_div(q.M, t); r.tiles_n = ceil_div(q.N, t / feat); r.split = (int)split; r.begin = (int)units;
-      r.out = p;
       r.dst = q.out;
       r.part = (float*)off;  // an offset until the launch knows the workspace
     }

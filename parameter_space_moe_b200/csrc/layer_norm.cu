@@ -11,8 +11,7 @@
 // the stored r, so that no caller has to keep them.
 //
 // Bounds.  Forward: HBM (32768 x 2048 bf16 with the residual sum, 537 MB: 88 us, 0.93 of a copy's rate).  Gradients:
-// instructions and the latency of a row's four sums, with the columns' sums holding 128 registers a thread (8192 x 768
-// bf16 / f32, 88 MB: 25 us with the partial sums' launch, 0.54 of a copy's rate).
+// instructions and the latency of a row's four sums at 128 registers a thread, two blocks an SM (8192 x 768 bf16 / f32, 88 MB: 25 us with the partial sums' launch, 0.54 of a copy's rate).
 // Few rows: one launch's latency (256 x 2048: 3.2 us on the GPU).
 #include "block_common.cuh"
 

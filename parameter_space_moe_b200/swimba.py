@@ -249,7 +249,6 @@ def out_proj(d, y, w_out, out, stream=None):
 # unless one is given.
 
 _TORCH = {F32: torch.float32, BF16: torch.bfloat16, F16: torch.float16}
-_NBYTES = {F32: 4, BF16: 2, F16: 2}
 
 
 def norm_dims(rows, width, dtype, grad_dtype=None, x_stride=0, eps=1e-5):
