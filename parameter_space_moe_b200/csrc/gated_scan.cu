@@ -189,12 +189,15 @@ __device__ __forceinline__ Map<V> send(Maps<V>& sm, int round, int warp, int lan
 }
 
 // Takes round `round`'s maps: returns the carried value in front of this warp's tokens and advances `carry` over the
-// round.
+// round.  A thread whose wait gave up waits no more (`waits`): all its rounds together are bounded like one.
 template <int V>
 __device__ __forceinline__ Vec<V> receive(Maps<V>& sm, int round, int lane, uint32_t rank, uint32_t nrank,
-                                          const Map<V>& before, Vec<V>& carry, unsigned* st) {
+                                          const Map<V>& before, Vec<V>& carry, bool& waits, unsigned* st) {
   const int buf = round & 1;
-  if (!wait_cluster(&sm.bar[buf], (uint32_t)(round >> 1) & 1u)) atomicOr(st, ST_TIMEOUT);
+  if (waits && !wait_cluster(&sm.bar[buf], (uint32_t)(round >> 1) & 1u)) {
+    waits = false;
+    atomicOr(st, ST_TIMEOUT);
+  }
   Vec<V> c = carry, at = carry;
   const Map<V>* m = sm.cta[buf][0] + lane;
   for (uint32_t r = 0; r < nrank; ++r, m += 32) {
@@ -305,6 +308,7 @@ gated_scan_kernel(int T_, int W, int ngrp, long long xs, long long gs, const T* 
   for (int k = 0; k < (kAsync ? kStages - 1 : 1); ++k) fetch(t + k * span, k);
   Vec<V> carry = load_state<V>(init, state, live);
   exchange_init(sm);
+  bool waits = true;
   int st = 0;
   for (int round = 0; round * span < T_; ++round, t += span) {
     if (kAsync) {
@@ -337,7 +341,7 @@ gated_scan_kernel(int T_, int W, int ngrp, long long xs, long long gs, const T* 
     mine.a = P[S - 1];
     mine.b = H[S - 1];
     const Map<V> before = send(sm, round, warp, lane, rank, nrank, mine);
-    const Vec<V> c = receive(sm, round, lane, rank, nrank, before, carry, status);
+    const Vec<V> c = receive(sm, round, lane, rank, nrank, before, carry, waits, status);
     T* out = h + (size_t)t * W;
     auto put = [&](int n) {
 #pragma unroll
@@ -406,6 +410,7 @@ gated_scan_bwd_kernel(int T_, int W, int ngrp, long long xs, long long gs, const
   for (int k = 0; k < (kAsync ? kStages - 1 : 1); ++k) fetch(t - k * span, k);
   Vec<V> carry = load_state<V>(dfinal, state, live);
   exchange_init(sm);
+  bool waits = true;
   int st = 0;
   for (int round = 0; round * span < T_; ++round, t -= span) {
     if (kAsync) {
@@ -437,7 +442,7 @@ gated_scan_bwd_kernel(int T_, int W, int ngrp, long long xs, long long gs, const
     for (int i = 1; i < S; ++i) then(mine, f[i], f[i] * d[i]);
     if (!kAsync) fetch(t - span, 0);
     const Map<V> before = send(sm, round, warp, lane, rank, nrank, mine);
-    Vec<V> c = receive(sm, round, lane, rank, nrank, before, carry, status);
+    Vec<V> c = receive(sm, round, lane, rank, nrank, before, carry, waits, status);
 #pragma unroll
     for (int i = 0; i < S; ++i) {
       const Vec<V> lam = d[i] + c;
@@ -503,7 +508,8 @@ void set_cluster(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr, int c, int 
 // on the fullest SM, and 0.02 us for every CTA of the cluster (fitted to sweeps of 1 .. 16 CTAs over 1 x 32768 x 2048,
 // 4 x 2048 x 1536, 1 x 30000 x 64, 1 x 20000 x 512 and odd widths; the parts stand beside the kernels' ways below).
 // Clusters are placed as densely as they fit, so the launch asks for as much shared memory as lets only its share fit an
-// SM (at 4 x 2048 x 1536, 384 CTAs: 23 us with three per SM, 30 us where four fitted and SMs stayed empty).  kFit: CTAs
+// SM (at 4 x 2048 x 1536, 384 CTAs: 23 us with three per SM, 30 us where four fitted and SMs stayed empty); while the scan
+// runs, kernels of other streams that use shared memory stay off the SMs it holds.  kFit: CTAs
 // that fit at 1 .. 4 per SM by cluster size; GPCs of uneven size hold fewer of the larger ones.
 struct Split {
   int c, per_sm;
