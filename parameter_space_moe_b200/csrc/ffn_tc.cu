@@ -186,6 +186,9 @@ ffn_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
     tc::fence_barrier_init();
   }
   griddep_launch_dependents();
+  // TMEM is taken ahead of the wait below.  A kernel that holds TMEM while it waits for one that still has to take its own
+  // on the same SM would stop both; the shared memory of this one leaves an SM no room for another of the library's kernels.
+  static_assert(233472 - (kSmemBytes + 1024) < 2048, "a CTA has its SM's shared memory to itself");
   if (warp == 1) {
     if (kPair) {
       tc::tmem_alloc_pair(tmem_slot, kTmemCols);
