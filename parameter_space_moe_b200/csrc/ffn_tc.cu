@@ -5,7 +5,7 @@
 // boxes along K for an operand stored along K, two along M or N for one stored across, which the MMA then reads
 // MN-major.  So no operand is ever transposed in memory and one tensor map per tensor serves every role.
 //   tile        256 x 256 by a CTA pair (cta_group::2, M256 N256 K16: each CTA loads 128 rows of A and 128 of B), or
-//               128 x 128 by one CTA where pairs would leave SMs without work
+//               128 x 128 by one CTA where all of them then run in one turn (make_plan)
 //   warp 0      TMA producer: A 32 KB + B 32 KB per 128-wide K slice, a ring of kStages
 //   warp 1      TMEM owner and MMA issuer, two accumulators in TMEM
 //   warps 2..9  epilogue from TMEM: a thread holds one row, 32 columns at a time; each warp stages its 32 x 32 block
@@ -494,6 +494,10 @@ Plan make_plan(const FfnLaunch& l, Args* a) {
   auto tiles = [&](const FfnProblem& q, int t) { return (long long)ceil_div(q.M, t) * ceil_div(q.N, t / feat); };
   long long big = 0;
   for (int p = 0; p < l.nprob; ++p) big += tiles(l.prob[p], 256);
+  // Up to 36 tiles of 256 x 256, four times as many of 128 x 128 run side by side on the SMs, which is the faster way; from
+  // 37 on they would take a second turn, and pairs are, though some SMs idle.  Pair against one CTA, us: gate and up at
+  // 256 x 2048 x 4608 (36 tiles) 19.3, 16.0, x 5632 (44) 19.8, 24.5; 1024 x 768 x 640 (20) 11.4, 9.1, x 1280 (40) 11.8, 12.9;
+  // dgate and dup at 1024 x 2048 x 2048 (32) 24.7, 17.5, 52 tiles 25.6, 27.9; the gradients at 2048 x 768 x 1024 (60) 19.0, 23.4.
   pl.pair = big >= kSms / 4;
   const int t = pl.pair ? 256 : 128, slots = pl.pair ? kSms / 2 : kSms;
   // A launch with fewer tiles than slots is split along K into units of about the same length, as long as each has two K
