@@ -17,8 +17,8 @@
 // Bounds.  Not HBM alone: a round is loads, maps, the exchange across the cluster and the replay, and the registers that
 // hold its tokens leave 8 to 16 warps an SM to hide one behind another.  bf16: 1 x 32768 x 2048 (403 MB) 104 us, 0.59 of a
 // copy's rate with 42 % of the issue slots used (21 instructions an element); 4 x 2048 x 1536 (75 MB) 23 us; its gradients
-// (151 MB) 38 us.  The step reads and writes the state once: 256 x 4096 bf16, 3.6 us on the GPU with state and rows in L2,
-// 6.0 us from HBM.
+// (151 MB) 38 us; captured passes over sets of inputs in turn, larger than L2 together, a user's calls on new inputs 1 to
+// 9 % more.  The step reads and writes the state once: 256 x 4096 bf16 4.6 us so, 3.6 us with state and rows in L2.
 #include <atomic>
 
 #include "block_common.cuh"
@@ -506,7 +506,9 @@ void set_cluster(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr, int c, int 
 // CTAs per cluster, a power of two, and CTAs per SM.  The cluster size is the one with the least estimated time: for every
 // set of clusters that is resident together 2.5 us and its rounds in a row, a round being a fixed part, one for every CTA
 // on the fullest SM, and 0.02 us for every CTA of the cluster (fitted to sweeps of 1 .. 16 CTAs over 1 x 32768 x 2048,
-// 4 x 2048 x 1536, 1 x 30000 x 64, 1 x 20000 x 512 and odd widths; the parts stand beside the kernels' ways below).
+// 4 x 2048 x 1536, 1 x 30000 x 64, 1 x 20000 x 512 and odd widths; the parts stand beside the kernels' ways below).  At 16
+// sizes outside those sweeps (1 x 12000 x 512 to 16 x 256 x 768, every type, odd widths, forward and gradients) it takes
+// at most 2 % more than the best of all cluster sizes and both ways.
 // Clusters are placed as densely as they fit, so the launch asks for as much shared memory as lets only its share fit an
 // SM (at 4 x 2048 x 1536, 384 CTAs: 23 us with three per SM, 30 us where four fitted and SMs stayed empty); while the scan
 // runs, kernels of other streams that use shared memory stay off the SMs it holds.  kFit: CTAs

@@ -10,9 +10,11 @@
 // normalised from the fp32 sum, not from the rounded r.  The backward pass takes the statistics again from
 // the stored r, so that no caller has to keep them.
 //
-// Bounds.  Forward: HBM (32768 x 2048 bf16 with the residual sum, 537 MB: 88 us, 0.93 of a copy's rate).  Gradients:
-// instructions and the latency of a row's four sums at 128 registers a thread, two blocks an SM (8192 x 768 bf16 / f32, 88 MB: 25 us with the partial sums' launch, 0.54 of a copy's rate).
-// Few rows: one launch's latency (256 x 2048: 3.2 us on the GPU).
+// Bounds.  Times are of captured passes over sets of inputs in turn, larger than L2 together; in brackets a user's calls on
+// inputs written in between, whose lines then leave L2 beside the pass.  Forward: HBM (32768 x 2048 bf16 with the residual
+// sum, 537 MB: 90 us, 0.91 of a copy's rate; [100 us, 0.82]).  Gradients: instructions and the latency of a row's four sums
+// at 128 registers a thread, two blocks an SM (8192 x 768 bf16 / f32, 88 MB: 22.7 us with the partial sums' launch, 0.59 of
+// a copy's rate; [24.6 us]).  Few rows: one launch's latency (256 x 2048: 3.5 us; [8 us, the host's call]).
 #include "block_common.cuh"
 
 namespace swimba {
@@ -21,11 +23,13 @@ namespace {
 
 // A row belongs to a team of whole warps, thread i of which holds the vectors i, i + team, ... of VEC columns; a block is
 // as many teams as its threads allow.  Sums over a warp and addresses cost the same for few columns a thread as for many;
-// more threads hide more latency.  Columns of a thread, at most (M x D, dtype / gradients' dtype, measured):
+// more threads hide more latency.  Columns of a thread, at most (M x D, dtype / gradients' dtype; both sides of a choice
+// measured on the same inputs again and again, the ones taken within 3 % of that over sets in turn):
 //   forward            16   32768 x 2048 bf16 with the residual sum: 88 us; 24 columns 102 us
 //     of odd widths     8   20000 x 1001 bf16 with the residual sum: 62 us; 16 columns (spills) 94 us
-//   16-bit gradients   16   8192 x 768 bf16 / f32 (12 columns): 25 us; 8 columns 32 us.  20000 x 2048 bf16 (16 columns,
-//                           one block of 384 threads an SM, whose registers do not spill): 94 us; two of 256 96 us
+//   16-bit gradients   16   8192 x 768 bf16 / f32 (12 columns): 25 us before gamma was kept; 8 columns 32 us.  20000 x 2048
+//                           bf16 (16 columns, one block of 384 threads an SM, whose registers do not spill): 94 us; two
+//                           of 256 96 us
 //   f32 gradients       8   5000 x 1500: 35 us with the rows ahead in shared memory; 16 in registers 45 us
 //     of odd widths     8   4099 x 1001 f32: 18 us with two blocks an SM; 4 columns 22 us, 8 with three (spills) 38 us
 // 8 where there are few rows, and 16, 24 or, in blocks of 512 threads, 32 where a block would not hold the row otherwise.
