@@ -20,9 +20,11 @@
 // (gate and up at K = 768: 46 us, pipe 56 %; dgate and dup with their two more inputs: 159 us, 63 %), and
 // turns that do not fill the SMs (8192 x 768 from K = 2048: 96 tiles on 74 pairs, 30.7 us, 41 %).  256 rows: the weights'
 // bytes and each launch's start and end (256 x 2048 x 5632, 74 MB: 21 + 14 + 5 us alone, 32 us together).
-// Persistent over the units (problem, tile, split of K); a product with few tiles or a very long K is split along K into
-// fp32 partial sums, added in a fixed order by a second kernel.
+// Persistent over the units (problem, tile, split of K); a product with few tiles is split along K into fp32
+// partial sums, added in a fixed order by a second kernel.
 #include <math.h>
+
+#include <type_traits>
 
 #include "ffn_act.cuh"
 #include "ffn_tc.cuh"
@@ -43,11 +45,14 @@ constexpr uint32_t kBlock = 32 * 64;                // an epilogue warp's staged
 constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + kEpiWarps * kBlocks * kBlock + 256;
 constexpr int kSms = 148;                           // what the plan fills; the launch asks the device
 constexpr int kMaxSplit = 16;                       // of a product with few tiles
-// K blocks of one accumulation of 16-bit operands, at most.  The tensor cores cut what an addition shifts out: 1.1e-7 of
-// the sum for every 16 of K when all terms have one sign.  Over 2^20 rows in one chain the weights' gradients came out
-// 6.5e-3 small; 65536 of K leave 4.3e-4, a ninth of bf16's half step, 16384 1.1e-4, a quarter of fp16's
-// (the gradients at 32768 x 768 x 2048 fp16: 605 us in one chain, 636 us in two).
-constexpr int longest(int dtype) { return dtype == SWIMBA_BF16 ? 512 : 128; }
+// K blocks of one accumulation of 16-bit operands, at most (kFfnStore; the others sum over the model's width alone).  The
+// tensor cores cut what an addition shifts out: 1.1e-7 of the sum for every 16 of K when all terms have one sign.  Over
+// 2^20 rows in one chain the weights' gradients came out 6.5e-3 small; 65536 of K leave 4.3e-4, a ninth of bf16's half
+// step, 16384 1.1e-4, a quarter of fp16's.  Longer sums leave the accumulator as often and are added up in registers, in
+// a kernel of their own, since the registers cost shorter ones up to 5 % (17000 x 2048 x 5632, the gradients: 1.83 and
+// 1.93 ms at best).  32768 x 768 x 2048 fp16, the gradients: 588 us in one chain and so, 617 us as split sums, which take
+// workspace besides.
+constexpr int longest(bool bf16) { return bf16 ? 512 : 128; }
 
 struct Prob {
   int M, N, kbs, nkb, a_mn, b_mn;  // kbs: K blocks of a segment, nkb: of all
@@ -151,13 +156,14 @@ struct RowOf {
   }
 };
 
-template <bool kPair, int kEpi, int kAct, class T>
+template <bool kPair, int kEpi, int kAct, class T, bool kLong>
 __global__ void __launch_bounds__(kThreads, 1)
 ffn_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a) {
   constexpr int TM = kPair ? 256 : 128, TN = kPair ? 256 : 128;
   constexpr int kFeat = kEpi == kFfnGlu ? TN / 2 : TN;  // output columns of a tile
   constexpr uint32_t kTmemCols = 2 * TN;
-  constexpr int kChain = sizeof(T) == 4 ? 2 : 1 << 30;  // K blocks of one accumulation
+  constexpr bool kChains = sizeof(T) == 4 || kLong;     // several accumulations, added up in registers
+  constexpr int kChain = sizeof(T) == 4 ? 2 : kLong ? longest(std::is_same<T, __nv_bfloat16>::value) : 1 << 30;  // K blocks of one accumulation
   constexpr int kPart = kFeat / (kEpiWarps / 4);        // columns of a tile that one warp drains
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = tc::smem_u32(smem_raw);
@@ -389,7 +395,7 @@ ffn_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a)
         }
       };
       bool ok = true;
-      if constexpr (sizeof(T) == 4) {
+      if constexpr (kChains) {
         float v[kPart / 32][32], w[kEpi == kFfnGlu ? kPart / 32 : 1][32];
 #pragma unroll
         for (int c = 0; c < kPart / 32; ++c)
@@ -515,8 +521,6 @@ Plan make_plan(const FfnLaunch& l, Args* a) {
     const int kbs = ceil_div(q.K, BK), nkb = kbs * q.nseg;
     long long split = l.epi == kFfnStore && total < slots ? nkb / length : 1;
     split = split < 1 ? 1 : split > kMaxSplit ? kMaxSplit : split;
-    if (l.epi == kFfnStore && l.dtype != SWIMBA_F32 && split < ceil_div(nkb, longest(l.dtype)))
-      split = ceil_div(nkb, longest(l.dtype));
     if (a) {
       Prob& r = a->prob[p];
       r.M = q.M; r.N = q.N; r.kbs = kbs; r.nkb = nkb; r.a_mn = q.a_mn; r.b_mn = q.b_mn;
@@ -547,9 +551,9 @@ int device_sms() {
   return sms;
 }
 
-template <bool kPair, int kEpi, int kAct, class T>
+template <bool kPair, int kEpi, int kAct, class T, bool kLong>
 cudaError_t go(const Maps& maps, const Args& a, cudaStream_t s) {
-  auto kernel = ffn_tc_kernel<kPair, kEpi, kAct, T>;
+  auto kernel = ffn_tc_kernel<kPair, kEpi, kAct, T, kLong>;
   cudaError_t e = set_max_dynamic_smem((const void*)kernel, kSmemBytes);
   if (e != cudaSuccess) return e;
   const int slots = kPair ? device_sms() / 2 : device_sms();
@@ -559,9 +563,9 @@ cudaError_t go(const Maps& maps, const Args& a, cudaStream_t s) {
   return e;
 }
 
-template <int kEpi, int kAct, class T>
+template <int kEpi, int kAct, class T, bool kLong = false>
 cudaError_t go_pair(bool pair, const Maps& maps, const Args& a, cudaStream_t s) {
-  return pair ? go<true, kEpi, kAct, T>(maps, a, s) : go<false, kEpi, kAct, T>(maps, a, s);
+  return pair ? go<true, kEpi, kAct, T, kLong>(maps, a, s) : go<false, kEpi, kAct, T, kLong>(maps, a, s);
 }
 
 template <int kEpi, class T>
@@ -573,7 +577,10 @@ template <class T>
 cudaError_t go_type(const FfnLaunch& l, const Plan& pl, const Maps& maps, const Args& a, cudaStream_t s) {
   if (l.epi == kFfnGlu) return go_act<kFfnGlu, T>(l.act, pl.pair, maps, a, s);
   if (l.epi == kFfnDglu) return go_act<kFfnDglu, T>(l.act, pl.pair, maps, a, s);
-  cudaError_t e = go_pair<kFfnStore, SWIMBA_SILU, T>(pl.pair, maps, a, s);
+  bool is_long = false;
+  for (int p = 0; p < a.nprob; ++p) is_long |= ceil_div(a.prob[p].nkb, a.prob[p].split) > longest(l.dtype == SWIMBA_BF16);
+  cudaError_t e = is_long ? go_pair<kFfnStore, SWIMBA_SILU, T, sizeof(T) == 2>(pl.pair, maps, a, s)
+                          : go_pair<kFfnStore, SWIMBA_SILU, T>(pl.pair, maps, a, s);
   if (e != cudaSuccess || !pl.split_any) return e;
   size_t most = 0;
   for (int p = 0; p < a.nprob; ++p)

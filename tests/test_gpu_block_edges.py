@@ -222,7 +222,7 @@ def test_gradients_of_the_weights_over_many_rows(M, D, F, dt):
         want_u += dup.T @ x[j].double()
         rough += dup.abs().T @ x[j].double().abs()
     # every term is positive, so a chain's running sum never passes its end: a step of 16 cuts less than 2^-23 of it, and
-    # a chain is 65536 of K (bf16) or 16384 (fp16) long; the split sums, 64 at most, add a rounding each
+    # a chain is 65536 of K (bf16) or 16384 (fp16) long; the sums of the chains, 64 at most, add a rounding each
     cut = (4096 if dt == "bf16" else 1024) * 2.0 ** -23 + 64 * U
     want = want_d.cpu().numpy()
     within(dwd.np(), want, cut * np.abs(want), t, f"dw_down {M}x{D}x{F} {dt}")
